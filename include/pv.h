@@ -71,6 +71,14 @@ typedef int pv_status;
 #define PV_MAX_RING    64
 #define PV_MAX_STREAMS 64
 
+/* Sparse attention reads keys in blocks of PV_BLOCK_KEYS inside one latent
+ * frame and chooses them for groups of PV_BLOCK_QUERIES queries. */
+#define PV_BLOCK_KEYS    128
+#define PV_BLOCK_QUERIES 256
+/* Blocks that pv_block_select takes whatever their score. */
+#define PV_FORCE_SINK    1  /* the sink's */
+#define PV_FORCE_CURRENT 2  /* the current chunk's */
+
 /* Phases of one stream (model card, "Inference profile"). */
 #define PV_PHASE_NEW    0  /* no chunk yet */
 #define PV_PHASE_FIRST  1  /* the first chunk (F0 frames) is being denoised */
@@ -140,6 +148,65 @@ PV_API pv_status pv_kv_init(pv_kv* out, const pv_kv_config* cfg, void* kv_dev, s
                      void* ws_dev, size_t ws_bytes);
 PV_API pv_status pv_kv_destroy(pv_kv kv);
 
+/* A paged store: the same handle and calls, but the streams share n_pages
+ * pages of one latent frame (T rows) instead of owning (F0 + R) frames each,
+ * so that streams branched from one another hold their common history once.
+ * A page id stands for the same rows in every layer, step and head:
+ * each (layer, step) is [H][n_pages * T][D].
+ *  - pv_kv_begin_chunk takes the pages: F0 consecutive ones for the first
+ *    chunk (the sink's), later the slot's own page again, or a free one when
+ *    the slot has none or its page is shared.  Free pages are taken lowest
+ *    first.  Too few: PV_ERR_CAPACITY, the state unchanged.
+ *  - pv_rope_append, pv_qkv_rope_append and pv_block_summarize write the
+ *    current chunk's page(s) and return PV_ERR_STATE while another stream
+ *    holds them too.
+ *  - pv_kv_set_state keeps the pages of frames that stay and takes free ones
+ *    for the others (contents are the caller's to restore).
+ *  - pv_chunk_attn reads through the page table; rows behind a frame's end
+ *    are never read.
+ * Page ids enter a launch by value: a captured launch keeps the pages that
+ * its streams held when it was captured.
+ * kv_bytes: 2 * layers * steps * H * n_pages * T * D bf16.  n_pages >= F0. */
+PV_API pv_status pv_kv_paged_required_bytes(const pv_kv_config* cfg, int n_pages,
+                                            size_t* kv_bytes, size_t* ws_bytes);
+PV_API pv_status pv_kv_init_paged(pv_kv* out, const pv_kv_config* cfg, int n_pages, void* kv_dev,
+                                  size_t kv_bytes, void* ws_dev, size_t ws_bytes);
+
+/* Makes each of dst[n_dst] (distinct streams in PV_PHASE_NEW) a branch of
+ * `src`: its schedule position and history.
+ *  Paged store: the history is shared, nothing is copied, except that with
+ *  copy_current != 0 each branch gets its own copy of the current chunk's
+ *  page(s) (the sink's F0 pages while the first chunk or the sink pass is
+ *  current), so that src and every branch can go on denoising it.  With 0
+ *  the current chunk should be complete; its page is shared until a holder
+ *  moves on.
+ *  Fixed rows: every key that src holds is copied (copy_current is ignored).
+ * Block means, where attached, are copied with the keys.  The copies are
+ * asynchronous on cuda_stream; calls of the handle issued on another stream
+ * must be ordered after them by the caller.  Too few pages: PV_ERR_CAPACITY,
+ * nothing changed. */
+PV_API pv_status pv_kv_fork(pv_kv kv, int src, int n_dst, const int* dst, int copy_current,
+                            void* cuda_stream);
+
+/* Ends `stream`: back to PV_PHASE_NEW; pages that no other stream holds are
+ * free.  Host only: launches that still read them must be ordered before
+ * later ones that write them, as on one CUDA stream they are. */
+PV_API pv_status pv_kv_release(pv_kv kv, int stream);
+
+/* Slides the held pages of a paged store down to the lowest ids, in their
+ * order, so that the free ones form one run (a first chunk needs F0
+ * consecutive ones).  Keys, and block means where attached, are moved on
+ * cuda_stream and every stream's page table follows; *moved (optional)
+ * counts the pages moved.  Fixed rows: nothing to do. */
+PV_API pv_status pv_kv_compact(pv_kv kv, int* moved, void* cuda_stream);
+
+/* Pages of `stream`: the first of the sink's F0 consecutive ones and
+ * pages[PV_MAX_RING], one per ring slot (-1: none).  PV_ERR_STATE for fixed
+ * rows. */
+PV_API pv_status pv_kv_page_table(pv_kv kv, int stream, int* sink_page, int* pages);
+/* Free pages of a paged store and the longest run of them. */
+PV_API pv_status pv_kv_free_pages(pv_kv kv, int* n_free, int* longest_run);
+
 /* Starts the next chunk of `stream` (model card, "Inference profile": the
  * first chunk has F0 frames, every later one 1 frame).  NEW -> FIRST needs
  * nframes == F0; BOOT or STEADY -> STEADY needs nframes == 1 and advances j,
@@ -159,7 +226,9 @@ PV_API pv_status pv_kv_set_state(pv_kv kv, int stream, const pv_kv_state* st);
 
 /* Element offsets (in bf16 units from kv_dev) of key row `key` of
  * (layer, step, stream, head) in the K and the V region.  step is 0..steps-1.
- * Rows 0..F0*T-1 are the sink, row F0*T + slot*T + t is token t of a slot. */
+ * Rows 0..F0*T-1 are the sink, row F0*T + slot*T + t is token t of a slot.
+ * Paged store: where the page table puts that row; PV_ERR_STATE for a frame
+ * that the stream holds no page for. */
 PV_API pv_status pv_kv_row_offset(pv_kv kv, int layer, int step, int stream, int head, int key,
                            size_t* k_elem, size_t* v_elem);
 
@@ -232,6 +301,79 @@ PV_API pv_status pv_qkv_rope_append(pv_kv kv, int n_streams, const int* streams,
  *  Computes in bf16 on the tensor cores with f32 accumulation and softmax. */
 PV_API pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
                         const void* q_rot, void* out, float* lse, void* cuda_stream);
+
+/* ------------------------------------------------------- sparse attention
+ * The keys of a sequence are cut into blocks of PV_BLOCK_KEYS: in a store
+ * inside each latent frame (ceil(T / 128) blocks per frame, bps below, the
+ * last one of T - 128 (bps - 1) keys), in explicit buffers over the n_k keys.
+ * Block b of a stream is block b % bps of frame b / bps, frames counted as
+ * key rows are: F0 sink frames, then the ring slots.  Every group of
+ * PV_BLOCK_QUERIES consecutive queries (the last one shorter) attends in each
+ * head to the blocks of a list of its own:
+ *  1. pv_block_summarize   mean key of each block, after the append;
+ *  2. pv_block_select      the `keep` best blocks of each (head, group);
+ *  3. pv_block_attn        softmax attention over the listed blocks.
+ * Lists are int32 [rows][keep], one row per (stream, head, group): stream
+ * i's rows start at H * (sum_{i'<i} G_i') and are [H][G_i], G = ceil(n_q / 256). */
+
+/* Bytes of the handle's block means: f32 [layers][steps][streams][H]
+ * [(F0 + R) * bps][D], for a paged store [layers][steps][H][n_pages * bps][D]. */
+PV_API pv_status pv_kv_summary_bytes(pv_kv kv, size_t* bytes);
+/* Attaches (NULL: detaches) a caller-owned buffer for the block means,
+ * 256-byte aligned, and zero-fills it (synchronous).  Until the handle is
+ * destroyed or the buffer detached, pv_block_summarize and page copies write it. */
+PV_API pv_status pv_kv_set_summaries(pv_kv kv, void* summ_dev, size_t bytes);
+
+/* Mean key of every block that the listed streams' current chunks hold at
+ * (layer, step), as pv_rope_append wrote them (PV_STEP_SINK: in every step
+ * buffer).  The sum of a block is taken in f64 and the mean rounded once to
+ * f32.  PV_ERR_STATE without attached means. */
+PV_API pv_status pv_block_summarize(pv_kv kv, int n_streams, const int* streams, int layer,
+                                    int step, void* cuda_stream);
+
+/* For each (stream, head, group): the min(keep, n_blocks) blocks of the
+ * stream's keys at (layer, step) whose mean key has the largest inner product
+ * with the group's mean query (mean rounded to f32, product in f64; equal
+ * scores: lowest block first; NaN scores last), as ascending block indices,
+ * -1 behind them.
+ *  force: PV_FORCE_* bits: blocks taken before any other while the stream is
+ *    in PV_PHASE_STEADY (elsewhere nothing is forced); more of them than
+ *    keep: PV_ERR_SHAPE.
+ *  q_rot: as for pv_chunk_attn.  blocks: int32 [rows][keep] output.
+ * At most 16384 blocks per stream, else PV_ERR_SHAPE. */
+PV_API pv_status pv_block_select(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                                 const void* q_rot, int keep, int force, int* blocks,
+                                 void* cuda_stream);
+
+/* pv_chunk_attn restricted to the first min(keep, n_blocks) entries of each
+ * list row.  An index outside 0..n_blocks-1 (such as -1) stands for an empty
+ * block; an index listed twice counts twice; a row without any key gives
+ * out = 0 and lse = -inf.  P is rounded to nearest bf16, its sum is not
+ * rounded.  Uses the handle's workspace, as pv_chunk_attn does. */
+PV_API pv_status pv_block_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                               const void* q_rot, const int* blocks, int keep, void* out,
+                               float* lse, void* cuda_stream);
+
+/* The same three on explicit head-major buffers, one sequence of 1 <= n_q,
+ * n_k <= 2^30 with H * n_q, H * n_k < 2^31 (else PV_ERR_SHAPE), blocks over
+ * the n_k keys (nb = ceil(n_k / 128)):
+ *  k, v [H][n_k][D] and q [H][n_q][D] bf16, means f32 [H][nb][D],
+ *  blocks int32 [H][ceil(n_q / 256)][keep], out bf16 [n_q][H][D],
+ *  lse optional f32 [n_q][H].  n_front (0..keep): the first blocks, always
+ *  taken.  ws: pv_block_attn_dense_ws_bytes, 256-byte aligned, zero-filled
+ *  before its first use, for one launch at a time; its first int is the
+ *  device error word, as for pv_attn_dense. */
+PV_API pv_status pv_block_summarize_dense(const void* k, int n_k, int heads, int head_dim,
+                                          float* means, void* cuda_stream);
+PV_API pv_status pv_block_select_dense(const void* q, const float* means, int n_q, int n_k,
+                                       int heads, int head_dim, int keep, int n_front, int* blocks,
+                                       void* cuda_stream);
+PV_API pv_status pv_block_attn_dense_ws_bytes(int n_q, int n_k, int heads, int head_dim, int keep,
+                                              size_t* ws_bytes);
+PV_API pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n_q, int n_k,
+                                     int heads, int head_dim, const int* blocks, int keep,
+                                     void* out, float* lse, void* ws, size_t ws_bytes,
+                                     void* cuda_stream);
 
 /* 3D RoPE over a whole clip of n_tokens = nframes * T tokens starting at
  * latent frame frame0, with the handle's geometry and table (for full

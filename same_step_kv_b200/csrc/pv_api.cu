@@ -52,7 +52,13 @@ struct StreamState {
     int fill = 0;
     int slot = -1;
     int slot_frame[PV_MAX_RING];
-    StreamState() { std::fill(slot_frame, slot_frame + PV_MAX_RING, -1); }
+    // paged store: first page of the sink's run, page of each ring slot
+    int sink_page = -1;
+    int page[PV_MAX_RING];
+    StreamState() {
+        std::fill(slot_frame, slot_frame + PV_MAX_RING, -1);
+        std::fill(page, page + PV_MAX_RING, -1);
+    }
 };
 
 // Workspace layout: [error word | counters | projection flags | RoPE table |
@@ -88,7 +94,8 @@ WsLayout ws_layout(const pv_kv_config& c) {
     return w;
 }
 
-pv_status check_config(const pv_kv_config* c) {
+// n_pages: pages of a paged store, 0 for fixed rows.
+pv_status check_config(const pv_kv_config* c, int n_pages = 0) {
     if (!c) return fail(PV_ERR_INVALID_ARG, "config is NULL");
     if (c->head_dim != 64 && c->head_dim != 128)
         return fail(PV_ERR_SHAPE, "head_dim %d: only 64 and 128 are supported", c->head_dim);
@@ -116,9 +123,14 @@ pv_status check_config(const pv_kv_config* c) {
     if (c->max_frames > kMaxFramesCfg)
         return fail(PV_ERR_SHAPE, "max_frames %d above %d", c->max_frames, kMaxFramesCfg);
     const int T = tokens_per_frame(*c);
-    const long long ltot = (long long)(c->first_frames + c->ring_slots) * T;
-    const long long rows = (long long)c->layers * c->steps * c->max_streams * c->heads * ltot;
-    if (rows >= (1LL << 31) || (long long)c->first_frames * T * c->heads >= (1LL << 30))
+    const long long ltot =
+        (long long)(n_pages > 0 ? n_pages : c->first_frames + c->ring_slots) * T;
+    const int sets = n_pages > 0 ? 1 : c->max_streams;
+    const long long rows = (long long)c->layers * c->steps * sets * c->heads * ltot;
+    if ((long long)(c->first_frames + (long long)c->ring_slots) * T >= (1LL << 31))
+        return fail(PV_ERR_SHAPE, "sink and ring of one stream hold 2^31 keys or more");
+    if (ltot >= (1LL << 31) || (double)c->layers * c->steps * sets * c->heads * (double)ltot >= 1e18 ||
+        rows >= (1LL << 31) || (long long)c->first_frames * T * c->heads >= (1LL << 30))
         return fail(PV_ERR_SHAPE, "store of %lld rows exceeds the 2^31 rows a tensor map addresses",
                     rows);
     if (c->first_frames - 1 + 1 > c->max_frames)
@@ -208,6 +220,30 @@ bool encode_out_map(CUtensorMap* map, void* out, long long tokens, int heads, in
     return true;
 }
 
+bool encode_seg_map(CUtensorMap* map, const void* base, int seg_len, long long segs, int D,
+                    char* err, size_t errlen) {
+    auto enc = get_encode();
+    if (!enc) {
+        snprintf(err, errlen, "cuTensorMapEncodeTiled is not available from the driver");
+        return false;
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)seg_len, (cuuint64_t)segs};
+    cuuint64_t strides[2] = {(cuuint64_t)D * sizeof(bf16),
+                             (cuuint64_t)seg_len * D * sizeof(bf16)};
+    cuuint32_t box[3] = {64, (cuuint32_t)kKeyTile, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(err, errlen, "cuTensorMapEncodeTiled failed (%d) for %lld segments of %d x %d",
+                 (int)r, segs, seg_len, D);
+        return false;
+    }
+    return true;
+}
+
 bool encode_2d_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem_bytes,
                    long long cols, long long rows, int box_cols, int box_rows, char* err,
                    size_t errlen) {
@@ -236,14 +272,19 @@ bool encode_2d_map(CUtensorMap* map, const void* base, CUtensorMapDataType type,
 struct pv_kv_s {
     pv_kv_config cfg{};
     int T = 0;
-    int ltot = 0;
+    int ltot = 0;       // rows of a head in one plane: (F0 + R) * T, or n_pages * T
+    int n_pages = 0;    // 0: fixed rows per stream; else pages shared by the streams
     int n_sm = 148;
+    int dev = -1;       // CUDA device of the buffers
     bool device = false;
     bf16* kbase = nullptr;
     bf16* vbase = nullptr;
     char* ws = nullptr;
     WsLayout wl{};
     CUtensorMap tm_k{}, tm_v{};
+    // the same regions as segments of T rows (block attention)
+    CUtensorMap tm_k3{}, tm_v3{};
+    bool maps3 = false;
     // the K and V regions with 32-row boxes (stores of the fused projection)
     CUtensorMap tm_k32{}, tm_v32{};
     bool maps32 = false;
@@ -251,6 +292,9 @@ struct pv_kv_s {
     // bits, so that it never comes back to a value a stale flag may hold)
     unsigned long long qkv_epoch = 0;
     std::vector<StreamState> streams;
+    std::vector<int> ref;    // paged: streams that hold each page
+    std::vector<int> remap;  // paged: scratch of pv_kv_compact
+    float* summ = nullptr;   // block means, or NULL
     std::mutex mu;
     // cached tensor map of the last q_rot buffer
     const void* qmap_ptr = nullptr;
@@ -264,16 +308,83 @@ struct pv_kv_s {
 
 namespace {
 
+// Streams with rows of their own in a plane (layer, step).
+int row_sets(const pv_kv_s* kv) { return kv->n_pages > 0 ? 1 : kv->cfg.max_streams; }
+
 long long region_rows(const pv_kv_s* kv) {
     const pv_kv_config& c = kv->cfg;
-    return (long long)c.layers * c.steps * c.max_streams * c.heads * kv->ltot;
+    return (long long)c.layers * c.steps * row_sets(kv) * c.heads * kv->ltot;
 }
 
-// Row (of D elements) of key 0, head 0 of (layer, step, stream) in a region.
+// Row (of D elements) of row 0 of head 0 of (layer, step) in a region: key 0
+// of the stream, or page 0 of a paged store.
 long long base_row(const pv_kv_s* kv, int layer, int step, int stream) {
     const pv_kv_config& c = kv->cfg;
-    return (((long long)layer * c.steps + step) * c.max_streams + stream) * c.heads *
-           (long long)kv->ltot;
+    return (((long long)layer * c.steps + step) * row_sets(kv) + (kv->n_pages > 0 ? 0 : stream)) *
+           c.heads * (long long)kv->ltot;
+}
+
+// Segments (frames, or pages) of a head in one plane, and of a whole plane.
+int head_segs(const pv_kv_s* kv) { return kv->ltot / kv->T; }
+long long plane_segs(const pv_kv_s* kv) {
+    return (long long)row_sets(kv) * kv->cfg.heads * head_segs(kv);
+}
+int blocks_per_seg(const pv_kv_s* kv) { return (kv->T + kKeyTile - 1) / kKeyTile; }
+
+// Where segment `seg` of a stream lies: its frame, or the page that holds it
+// (-1: none).
+int page_of(const pv_kv_s* kv, const StreamState& s, int seg) {
+    if (kv->n_pages == 0) return seg;
+    const int f0 = kv->cfg.first_frames;
+    return seg < f0 ? (s.sink_page < 0 ? -1 : s.sink_page + seg) : s.page[seg - f0];
+}
+
+// ------------------------------------------------------------------ pages
+// The lowest run of n consecutive free pages, or -1.
+int find_pages(const pv_kv_s* kv, int n) {
+    int run = 0;
+    for (int i = 0; i < kv->n_pages; ++i) {
+        run = kv->ref[i] == 0 ? run + 1 : 0;
+        if (run == n) return i - n + 1;
+    }
+    return -1;
+}
+void hold_pages(pv_kv_s* kv, int page, int n, int by) {
+    for (int i = 0; i < n; ++i) kv->ref[page + i] += by;
+}
+void release_pages(pv_kv_s* kv, StreamState& s) {
+    if (kv->n_pages == 0) return;
+    if (s.sink_page >= 0) hold_pages(kv, s.sink_page, kv->cfg.first_frames, -1);
+    s.sink_page = -1;
+    for (int i = 0; i < kv->cfg.ring_slots; ++i) {
+        if (s.page[i] >= 0) --kv->ref[s.page[i]];
+        s.page[i] = -1;
+    }
+}
+pv_status no_pages(const pv_kv_s* kv, int n) {
+    int free_pages = 0;
+    for (int r : kv->ref) free_pages += r == 0;
+    return fail(PV_ERR_CAPACITY,
+                "no %d consecutive free pages (%d of %d free; release a stream or compact the store)",
+                n, free_pages, kv->n_pages);
+}
+// The pages that the stream's current chunk writes: first page and count.
+void current_pages(const pv_kv_s* kv, const StreamState& s, int* page, int* n) {
+    const bool sink = s.phase == PV_PHASE_FIRST || s.phase == PV_PHASE_BOOT;
+    *n = sink ? kv->cfg.first_frames : 1;
+    *page = sink ? s.sink_page : s.page[s.slot];
+}
+// A page that several streams hold is not written.
+pv_status check_owned(const pv_kv_s* kv, const StreamState& s, int stream) {
+    if (kv->n_pages == 0) return PV_OK;
+    int page, n;
+    current_pages(kv, s, &page, &n);
+    for (int i = 0; i < n; ++i)
+        if (kv->ref[page + i] > 1)
+            return fail(PV_ERR_STATE,
+                        "stream %d: its current chunk's page %d is shared (fork with copy_current, "
+                        "or start the next chunk)", stream, page + i);
+    return PV_OK;
 }
 
 void derive(const pv_kv_s* kv, const StreamState& s, pv_kv_state* o) {
@@ -338,6 +449,116 @@ pv_status out_map(pv_kv kv, void* out, long long tokens, CUtensorMap* map) {
     return PV_OK;
 }
 
+// Sizes of the buffers of a store of fixed rows (n_pages 0) or of n_pages pages.
+pv_status store_bytes(const pv_kv_config* cfg, int n_pages, size_t* kv_bytes, size_t* ws_bytes) {
+    pv_status st = check_config(cfg, n_pages);
+    if (st) return st;
+    if (!kv_bytes || !ws_bytes) return fail(PV_ERR_INVALID_ARG, "output pointer is NULL");
+    if (n_pages > 0 && n_pages < cfg->first_frames)
+        return fail(PV_ERR_SHAPE, "n_pages %d below the %d pages of a sink", n_pages,
+                    cfg->first_frames);
+    const size_t segs = n_pages > 0 ? (size_t)n_pages
+                                    : (size_t)cfg->max_streams * (cfg->first_frames + cfg->ring_slots);
+    *kv_bytes = 2 * (size_t)cfg->layers * cfg->steps * segs * cfg->heads * tokens_per_frame(*cfg) *
+                cfg->head_dim * sizeof(bf16);
+    *ws_bytes = ws_layout(*cfg).total;
+    return PV_OK;
+}
+
+pv_status store_init(pv_kv* out, const pv_kv_config* cfg, int n_pages, void* kv_dev,
+                     size_t kv_bytes, void* ws_dev, size_t ws_bytes) {
+    if (!out) return fail(PV_ERR_INVALID_ARG, "out handle pointer is NULL");
+    *out = nullptr;
+    pv_status st = check_config(cfg, n_pages);
+    if (st) return st;
+    const bool bookkeeping_only = (kv_dev == nullptr && ws_dev == nullptr);
+    if (!bookkeeping_only && (!kv_dev || !ws_dev))
+        return fail(PV_ERR_INVALID_ARG, "pass both device buffers, or neither");
+    size_t need_kv = 0, need_ws = 0;
+    if ((st = store_bytes(cfg, n_pages, &need_kv, &need_ws))) return st;
+    pv_kv_s* kv = new (std::nothrow) pv_kv_s();
+    if (!kv) return fail(PV_ERR_CAPACITY, "host allocation failed");
+    kv->cfg = *cfg;
+    kv->T = tokens_per_frame(*cfg);
+    kv->n_pages = n_pages;
+    kv->ltot = (n_pages > 0 ? n_pages : cfg->first_frames + cfg->ring_slots) * kv->T;
+    try {
+        kv->streams.resize(cfg->max_streams);
+        kv->ref.assign(n_pages, 0);
+        kv->remap.assign(n_pages, 0);
+    } catch (const std::bad_alloc&) {
+        delete kv;
+        return fail(PV_ERR_CAPACITY, "host allocation failed");
+    }
+    kv->wl = ws_layout(*cfg);
+    if (!bookkeeping_only) {
+        if (kv_bytes < need_kv || ws_bytes < need_ws) {
+            delete kv;
+            return fail(PV_ERR_CAPACITY, "buffers of %zu / %zu bytes, need %zu / %zu", kv_bytes,
+                        ws_bytes, need_kv, need_ws);
+        }
+        if (!aligned(kv_dev, 256) || !aligned(ws_dev, 256)) {
+            delete kv;
+            return fail(PV_ERR_INVALID_ARG, "device buffers must be 256-byte aligned");
+        }
+        if ((st = check_device(&kv->n_sm))) {
+            delete kv;
+            return st;
+        }
+        if (cudaGetDevice(&kv->dev) != cudaSuccess) kv->dev = -1;
+        kv->device = true;
+        kv->kbase = (bf16*)kv_dev;
+        kv->vbase = kv->kbase + (size_t)region_rows(kv) * cfg->head_dim;
+        kv->ws = (char*)ws_dev;
+        // RoPE table, fp64 on the host, stored as f32 (cos, sin).
+        const pv_kv_config& c = *cfg;
+        std::vector<float2> tab(kv->wl.n_table);
+        auto fill_axis = [&](int base, int npos, int npairs) {
+            for (int p = 0; p < npos; ++p)
+                for (int k = 0; k < npairs; ++k) {
+                    const double freq = std::pow(c.rope_theta, -2.0 * k / (2.0 * npairs));
+                    const double a = p * freq;
+                    tab[base + p * npairs + k] = make_float2((float)std::cos(a), (float)std::sin(a));
+                }
+        };
+        fill_axis(0, c.max_frames, c.rope_pairs_t);
+        fill_axis(c.max_frames * c.rope_pairs_t, c.frame_h, c.rope_pairs_h);
+        fill_axis(c.max_frames * c.rope_pairs_t + c.frame_h * c.rope_pairs_h, c.frame_w,
+                  c.rope_pairs_w);
+        cudaError_t e = cudaMemset(kv_dev, 0, need_kv);
+        if (e == cudaSuccess) e = cudaMemset(ws_dev, 0, need_ws);
+        if (e == cudaSuccess)
+            e = cudaMemcpy(kv->ws + kv->wl.tab_off, tab.data(), sizeof(float2) * tab.size(),
+                           cudaMemcpyHostToDevice);
+        if (e != cudaSuccess) {
+            delete kv;
+            return cuda_fail(e, "initialising the store");
+        }
+        char msg[256];
+        if (!encode_rows_map(&kv->tm_k, kv->kbase, region_rows(kv), c.head_dim, msg, sizeof msg) ||
+            !encode_rows_map(&kv->tm_v, kv->vbase, region_rows(kv), c.head_dim, msg, sizeof msg)) {
+            delete kv;
+            return fail(PV_ERR_CUDA, "%s", msg);
+        }
+        kv->maps3 = encode_seg_map(&kv->tm_k3, kv->kbase, kv->T, region_rows(kv) / kv->T,
+                                   c.head_dim, msg, sizeof msg) &&
+                    encode_seg_map(&kv->tm_v3, kv->vbase, kv->T, region_rows(kv) / kv->T,
+                                   c.head_dim, msg, sizeof msg);
+        if (n_pages > 0 && !kv->maps3) {
+            delete kv;
+            return fail(PV_ERR_CUDA, "%s", msg);
+        }
+        // without them pv_qkv_rope_append takes its two-launch path
+        kv->maps32 = region_rows(kv) < (1LL << 31) &&
+                     encode_2d_map(&kv->tm_k32, kv->kbase, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                   c.head_dim, region_rows(kv), 64, 32, msg, sizeof msg) &&
+                     encode_2d_map(&kv->tm_v32, kv->vbase, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                   c.head_dim, region_rows(kv), 64, 32, msg, sizeof msg);
+    }
+    *out = kv;
+    return PV_OK;
+}
+
 // Shape checks and sizes shared by pv_attn_varlen_ws_bytes and pv_attn_varlen.
 pv_status varlen_sizes(int n_seqs, const int* n_q, const int* n_k, int heads, int head_dim,
                        long long* tot_q, long long* tot_k, size_t* n_cnt, size_t* tiles) {
@@ -380,92 +601,26 @@ pv_status pv_last_error(char* buf, size_t len) {
 }
 
 pv_status pv_kv_required_bytes(const pv_kv_config* cfg, size_t* kv_bytes, size_t* ws_bytes) {
-    pv_status st = check_config(cfg);
-    if (st) return st;
-    if (!kv_bytes || !ws_bytes) return fail(PV_ERR_INVALID_ARG, "output pointer is NULL");
-    const int T = tokens_per_frame(*cfg);
-    const size_t ltot = (size_t)(cfg->first_frames + cfg->ring_slots) * T;
-    *kv_bytes = 2 * (size_t)cfg->layers * cfg->steps * cfg->max_streams * cfg->heads * ltot *
-                cfg->head_dim * sizeof(bf16);
-    *ws_bytes = ws_layout(*cfg).total;
-    return PV_OK;
+    return store_bytes(cfg, 0, kv_bytes, ws_bytes);
+}
+
+pv_status pv_kv_paged_required_bytes(const pv_kv_config* cfg, int n_pages, size_t* kv_bytes,
+                                     size_t* ws_bytes) {
+    if (n_pages < 1) return fail(PV_ERR_SHAPE, "n_pages must be positive");
+    return store_bytes(cfg, n_pages, kv_bytes, ws_bytes);
 }
 
 pv_status pv_kv_init(pv_kv* out, const pv_kv_config* cfg, void* kv_dev, size_t kv_bytes,
                      void* ws_dev, size_t ws_bytes) {
+    return store_init(out, cfg, 0, kv_dev, kv_bytes, ws_dev, ws_bytes);
+}
+
+pv_status pv_kv_init_paged(pv_kv* out, const pv_kv_config* cfg, int n_pages, void* kv_dev,
+                           size_t kv_bytes, void* ws_dev, size_t ws_bytes) {
     if (!out) return fail(PV_ERR_INVALID_ARG, "out handle pointer is NULL");
     *out = nullptr;
-    pv_status st = check_config(cfg);
-    if (st) return st;
-    const bool bookkeeping_only = (kv_dev == nullptr && ws_dev == nullptr);
-    if (!bookkeeping_only && (!kv_dev || !ws_dev))
-        return fail(PV_ERR_INVALID_ARG, "pass both device buffers, or neither");
-    size_t need_kv = 0, need_ws = 0;
-    pv_kv_required_bytes(cfg, &need_kv, &need_ws);
-    pv_kv_s* kv = new (std::nothrow) pv_kv_s();
-    if (!kv) return fail(PV_ERR_CAPACITY, "host allocation failed");
-    kv->cfg = *cfg;
-    kv->T = tokens_per_frame(*cfg);
-    kv->ltot = (cfg->first_frames + cfg->ring_slots) * kv->T;
-    kv->streams.resize(cfg->max_streams);
-    kv->wl = ws_layout(*cfg);
-    if (!bookkeeping_only) {
-        if (kv_bytes < need_kv || ws_bytes < need_ws) {
-            delete kv;
-            return fail(PV_ERR_CAPACITY, "buffers of %zu / %zu bytes, need %zu / %zu", kv_bytes,
-                        ws_bytes, need_kv, need_ws);
-        }
-        if (!aligned(kv_dev, 256) || !aligned(ws_dev, 256)) {
-            delete kv;
-            return fail(PV_ERR_INVALID_ARG, "device buffers must be 256-byte aligned");
-        }
-        if ((st = check_device(&kv->n_sm))) {
-            delete kv;
-            return st;
-        }
-        kv->device = true;
-        kv->kbase = (bf16*)kv_dev;
-        kv->vbase = kv->kbase + (size_t)region_rows(kv) * cfg->head_dim;
-        kv->ws = (char*)ws_dev;
-        // RoPE table, fp64 on the host, stored as f32 (cos, sin).
-        const pv_kv_config& c = *cfg;
-        std::vector<float2> tab(kv->wl.n_table);
-        auto fill_axis = [&](int base, int npos, int npairs) {
-            for (int p = 0; p < npos; ++p)
-                for (int k = 0; k < npairs; ++k) {
-                    const double freq = std::pow(c.rope_theta, -2.0 * k / (2.0 * npairs));
-                    const double a = p * freq;
-                    tab[base + p * npairs + k] = make_float2((float)std::cos(a), (float)std::sin(a));
-                }
-        };
-        fill_axis(0, c.max_frames, c.rope_pairs_t);
-        fill_axis(c.max_frames * c.rope_pairs_t, c.frame_h, c.rope_pairs_h);
-        fill_axis(c.max_frames * c.rope_pairs_t + c.frame_h * c.rope_pairs_h, c.frame_w,
-                  c.rope_pairs_w);
-        cudaError_t e = cudaMemset(kv_dev, 0, need_kv);
-        if (e == cudaSuccess) e = cudaMemset(ws_dev, 0, need_ws);
-        if (e == cudaSuccess)
-            e = cudaMemcpy(kv->ws + kv->wl.tab_off, tab.data(), sizeof(float2) * tab.size(),
-                           cudaMemcpyHostToDevice);
-        if (e != cudaSuccess) {
-            delete kv;
-            return cuda_fail(e, "initialising the store");
-        }
-        char msg[256];
-        if (!encode_rows_map(&kv->tm_k, kv->kbase, region_rows(kv), c.head_dim, msg, sizeof msg) ||
-            !encode_rows_map(&kv->tm_v, kv->vbase, region_rows(kv), c.head_dim, msg, sizeof msg)) {
-            delete kv;
-            return fail(PV_ERR_CUDA, "%s", msg);
-        }
-        // without them pv_qkv_rope_append takes its two-launch path
-        kv->maps32 = region_rows(kv) < (1LL << 31) &&
-                     encode_2d_map(&kv->tm_k32, kv->kbase, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                                   c.head_dim, region_rows(kv), 64, 32, msg, sizeof msg) &&
-                     encode_2d_map(&kv->tm_v32, kv->vbase, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                                   c.head_dim, region_rows(kv), 64, 32, msg, sizeof msg);
-    }
-    *out = kv;
-    return PV_OK;
+    if (n_pages < 1) return fail(PV_ERR_SHAPE, "n_pages must be positive");
+    return store_init(out, cfg, n_pages, kv_dev, kv_bytes, ws_dev, ws_bytes);
 }
 
 pv_status pv_kv_destroy(pv_kv kv) {
@@ -485,6 +640,12 @@ pv_status pv_kv_begin_chunk(pv_kv kv, int stream, int nframes) {
             if (nframes != c.first_frames)
                 return fail(PV_ERR_STATE, "the first chunk holds %d frames, not %d",
                             c.first_frames, nframes);
+            if (kv->n_pages > 0) {
+                const int page = find_pages(kv, c.first_frames);
+                if (page < 0) return no_pages(kv, c.first_frames);
+                hold_pages(kv, page, c.first_frames, 1);
+                s.sink_page = page;
+            }
             s.phase = PV_PHASE_FIRST;
             s.chunk = 0;
             return PV_OK;
@@ -497,6 +658,17 @@ pv_status pv_kv_begin_chunk(pv_kv kv, int stream, int nframes) {
             if (c.first_frames + s.chunk + 1 > c.max_frames)
                 return fail(PV_ERR_CAPACITY, "chunk %d would reach latent frame %d >= max_frames %d",
                             s.chunk + 1, c.first_frames + s.chunk, c.max_frames);
+            if (kv->n_pages > 0) {
+                // the slot's own page again, or a fresh one in place of a shared one
+                int& page = s.page[s.chunk % c.ring_slots];
+                if (page < 0 || kv->ref[page] > 1) {
+                    const int fresh = find_pages(kv, 1);
+                    if (fresh < 0) return no_pages(kv, 1);
+                    if (page >= 0) --kv->ref[page];
+                    page = fresh;
+                    kv->ref[page] = 1;
+                }
+            }
             s.phase = PV_PHASE_STEADY;
             s.chunk += 1;
             s.slot = (s.chunk - 1) % c.ring_slots;
@@ -559,7 +731,43 @@ pv_status pv_kv_set_state(pv_kv kv, int stream, const pv_kv_state* st) {
             return fail(PV_ERR_STATE, "unknown phase %d", st->phase);
     }
     std::lock_guard<std::mutex> lock(kv->mu);
-    kv->streams[stream] = s;
+    StreamState& old = kv->streams[stream];
+    if (kv->n_pages > 0) {
+        // keep the pages of segments that stay, take free ones for the others;
+        // on failure give those back
+        s.sink_page = s.phase == PV_PHASE_NEW ? -1 : old.sink_page;
+        int fresh[PV_MAX_RING], n_fresh = 0;
+        int fresh_sink = -1;
+        bool ok = true;
+        if (s.phase != PV_PHASE_NEW && s.sink_page < 0) {
+            fresh_sink = find_pages(kv, c.first_frames);
+            if ((ok = fresh_sink >= 0)) {
+                hold_pages(kv, fresh_sink, c.first_frames, 1);
+                s.sink_page = fresh_sink;
+            }
+        }
+        int want = ok ? 1 : c.first_frames;
+        for (int i = 0; ok && i < s.fill; ++i) {
+            s.page[i] = old.page[i];
+            if (s.page[i] >= 0) continue;
+            const int page = find_pages(kv, 1);
+            if (!(ok = page >= 0)) break;
+            kv->ref[page] = 1;
+            s.page[i] = fresh[n_fresh++] = page;
+        }
+        if (!ok) {
+            const pv_status st2 = no_pages(kv, want);
+            if (fresh_sink >= 0) hold_pages(kv, fresh_sink, c.first_frames, -1);
+            for (int i = 0; i < n_fresh; ++i) --kv->ref[fresh[i]];
+            return st2;
+        }
+        // drop what the new state does not hold
+        if (s.sink_page < 0 && old.sink_page >= 0)
+            hold_pages(kv, old.sink_page, c.first_frames, -1);
+        for (int i = s.fill; i < c.ring_slots; ++i)
+            if (old.page[i] >= 0) --kv->ref[old.page[i]];
+    }
+    old = s;
     return PV_OK;
 }
 
@@ -568,9 +776,14 @@ pv_status pv_kv_row_offset(pv_kv kv, int layer, int step, int stream, int head, 
     if (!kv || !k_elem || !v_elem) return fail(PV_ERR_INVALID_ARG, "NULL argument");
     const pv_kv_config& c = kv->cfg;
     if (layer < 0 || layer >= c.layers || step < 0 || step >= c.steps || stream < 0 ||
-        stream >= c.max_streams || head < 0 || head >= c.heads || key < 0 || key >= kv->ltot)
+        stream >= c.max_streams || head < 0 || head >= c.heads || key < 0 ||
+        key / kv->T >= c.first_frames + c.ring_slots)
         return fail(PV_ERR_INVALID_ARG, "index outside the store");
-    const long long row = base_row(kv, layer, step, stream) + (long long)head * kv->ltot + key;
+    std::lock_guard<std::mutex> lock(kv->mu);
+    const int page = page_of(kv, kv->streams[stream], key / kv->T);
+    if (page < 0) return fail(PV_ERR_STATE, "stream %d holds no page for key %d", stream, key);
+    const long long row = base_row(kv, layer, step, stream) + (long long)head * kv->ltot +
+                          (long long)page * kv->T + key % kv->T;
     *k_elem = (size_t)row * c.head_dim;
     *v_elem = (size_t)(region_rows(kv) + row) * c.head_dim;
     return PV_OK;
@@ -600,6 +813,7 @@ pv_status rope_params(pv_kv kv, int n_streams, const int* streams, int layer, in
         } else if (s.phase != PV_PHASE_FIRST && s.phase != PV_PHASE_STEADY) {
             return fail(PV_ERR_STATE, "stream %d: no denoising step in phase %d", streams[i], s.phase);
         }
+        if ((st = check_owned(kv, s, streams[i]))) return st;
     }
     RopeParams& p = *pp;
     p.k_dst = kv->kbase;
@@ -626,16 +840,17 @@ pv_status rope_params(pv_kv kv, int n_streams, const int* streams, int layer, in
         sd.n_tok = d.n_queries;
         sd.frame0 = d.frame0;
         sd.qrot_row0 = (long long)c.heads * tok;
+        // the chunk's rows: the sink's (consecutive frames or pages), or the slot's
+        const long long at =
+            (long long)page_of(kv, s, s.phase == PV_PHASE_STEADY ? c.first_frames + s.slot : 0) *
+            kv->T;
         if (step == PV_STEP_SINK) {
             sd.n_dst = c.steps;
-            for (int s2 = 0; s2 < c.steps; ++s2) sd.dst_row0[s2] = base_row(kv, layer, s2, streams[i]);
-        } else if (s.phase == PV_PHASE_FIRST) {
-            sd.n_dst = 1;
-            sd.dst_row0[0] = base_row(kv, layer, step, streams[i]);
+            for (int s2 = 0; s2 < c.steps; ++s2)
+                sd.dst_row0[s2] = base_row(kv, layer, s2, streams[i]) + at;
         } else {
             sd.n_dst = 1;
-            sd.dst_row0[0] = base_row(kv, layer, step, streams[i]) +
-                             (long long)(c.first_frames + s.slot) * kv->T;
+            sd.dst_row0[0] = base_row(kv, layer, step, streams[i]) + at;
         }
         tok += d.n_queries;
         mt = std::max(mt, d.n_queries);
@@ -766,22 +981,109 @@ pv_status pv_qkv_rope_append(pv_kv kv, int n_streams, const int* streams, int la
     return PV_OK;
 }
 
-pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
-                        const void* q_rot, void* out, float* lse, void* cuda_stream) {
-    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
-    if (!kv->device) return fail(PV_ERR_STATE, "bookkeeping-only handle has no device buffers");
+}  // extern "C"
+
+namespace {
+// Checks shared by the calls that read a chunk's keys at (layer, step).
+pv_status check_read(pv_kv kv, int n_streams, const int* streams, int layer, int step) {
     pv_status st = check_streams(kv, n_streams, streams);
     if (st) return st;
     const pv_kv_config& c = kv->cfg;
     if (layer < 0 || layer >= c.layers) return fail(PV_ERR_INVALID_ARG, "layer %d out of range", layer);
     if (!(step == PV_STEP_SINK || (step >= 0 && step < c.steps)))
         return fail(PV_ERR_INVALID_ARG, "step %d is neither 0..%d nor PV_STEP_SINK", step, c.steps - 1);
+    return PV_OK;
+}
+pv_status check_read_phase(const StreamState& s, int stream, int step) {
+    if (step == PV_STEP_SINK) {
+        if (s.phase != PV_PHASE_BOOT)
+            return fail(PV_ERR_STATE, "stream %d: sink attention needs the sink pass first", stream);
+    } else if (s.phase != PV_PHASE_FIRST && s.phase != PV_PHASE_STEADY) {
+        return fail(PV_ERR_STATE, "stream %d: no denoising step in phase %d", stream, s.phase);
+    }
+    return PV_OK;
+}
+// The launches of a handle go to the device that holds its buffers.
+pv_status check_same_device(const pv_kv_s* kv) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev != kv->dev)
+        return fail(PV_ERR_INVALID_ARG, "the store lies on device %d, the current device is %d",
+                    kv->dev, dev);
+    return PV_OK;
+}
+
+// Block geometry of the listed streams at (layer, step).
+pv_status store_blocks(const pv_kv_s* kv, int n_streams, const int* streams, int layer, int step,
+                       KeyBlocks* kb) {
+    long long tok = 0;
+    kb->seg_len = kv->T;
+    kb->bps = blocks_per_seg(kv);
+    kb->tail = kv->T - (kb->bps - 1) * kKeyTile;
+    kb->head_segs = head_segs(kv);
+    kb->first = kv->cfg.first_frames;
+    for (int i = 0; i < n_streams; ++i) {
+        pv_kv_state d;
+        derive(kv, kv->streams[streams[i]], &d);
+        kb->seg0[i] = (int)(base_row(kv, layer, std::max(step, 0), streams[i]) / kv->T);
+        const long long n = (long long)(d.n_keys / kv->T) * kb->bps;
+        tok += d.n_queries;
+        if (n * kKeyTile > kMaxLen || tok * kv->cfg.heads >= (1LL << 31))
+            return fail(PV_ERR_SHAPE, "stream %d: %lld blocks, %lld tokens in the call: too many",
+                        streams[i], n, tok);
+        kb->n_blocks[i] = (int)n;
+    }
+    return PV_OK;
+}
+void fill_pages(const pv_kv_s* kv, int n_streams, const int* streams, PageTable* t) {
+    for (int i = 0; i < n_streams; ++i) {
+        const StreamState& s = kv->streams[streams[i]];
+        t->sink[i] = s.sink_page;
+        for (int r = 0; r < s.fill; ++r) t->ring[i][r] = s.page[r];
+    }
+}
+
+template <typename Pages>
+cudaError_t launch_store_blocks(pv_kv kv, const CUtensorMap& tq, const CUtensorMap& to,
+                                const AttnParams& p, const int* blocks, int keep,
+                                const int* list_row0, const KeyBlocks& kb, const Pages& pages,
+                                cudaStream_t s) {
+    BlockArgs<Pages> b{};
+    b.list = blocks;
+    b.keep = keep;
+    std::copy(list_row0, list_row0 + p.n_streams, b.list_row0);
+    b.kb = kb;
+    b.pages = pages;
+    return launch_block_attn(tq, kv->tm_k3, kv->tm_v3, to, p, b, s);
+}
+
+// Attention of the listed streams at (layer, step): over the listed blocks,
+// or over every key (blocks NULL).  Fixed rows without a list are contiguous
+// keys; everything else goes block by block.
+pv_status store_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                     const void* q_rot, const int* blocks, int keep, void* out, float* lse,
+                     void* cuda_stream) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    if (!kv->device) return fail(PV_ERR_STATE, "bookkeeping-only handle has no device buffers");
+    pv_status st = check_read(kv, n_streams, streams, layer, step);
+    if (st) return st;
+    const pv_kv_config& c = kv->cfg;
     if (!q_rot || !out) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
     if (!aligned(q_rot, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
         return fail(PV_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    const bool by_block = blocks || kv->n_pages > 0;
+    if (by_block && !kv->maps3) return fail(PV_ERR_SHAPE, "no tensor map of the store's frames");
+    if (by_block && (st = check_same_device(kv))) return st;
     if ((st = check_async("an earlier launch"))) return st;
 
     std::lock_guard<std::mutex> lock(kv->mu);
+    for (int i = 0; i < n_streams; ++i)
+        if ((st = check_read_phase(kv->streams[streams[i]], streams[i], step))) return st;
+    KeyBlocks kb{};
+    if (by_block && (st = store_blocks(kv, n_streams, streams, layer, step, &kb))) return st;
+    int list_row0[PV_MAX_STREAMS];
+    long long list_rows = 0;
     AttnParams p{};
     p.out = (bf16*)out;
     p.lse = lse;
@@ -794,23 +1096,20 @@ pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int layer, 
     p.n_streams = n_streams;
     int tok = 0;
     for (int i = 0; i < n_streams; ++i) {
-        const StreamState& s = kv->streams[streams[i]];
-        if (step == PV_STEP_SINK) {
-            if (s.phase != PV_PHASE_BOOT)
-                return fail(PV_ERR_STATE, "stream %d: sink attention needs the sink pass first",
-                            streams[i]);
-        } else if (s.phase != PV_PHASE_FIRST && s.phase != PV_PHASE_STEADY) {
-            return fail(PV_ERR_STATE, "stream %d: no denoising step in phase %d", streams[i], s.phase);
-        }
         pv_kv_state d;
-        derive(kv, s, &d);
+        derive(kv, kv->streams[streams[i]], &d);
         AttnStreamDesc& a = p.st[i];
+        a.id = i;
         a.n_q = d.n_queries;
-        a.n_k = d.n_keys;
+        // block by block, the plan counts the stream's tiles as full ones
+        a.n_k = !by_block ? d.n_keys
+                          : kKeyTile * (blocks ? std::min(keep, kb.n_blocks[i]) : kb.n_blocks[i]);
         a.q_row0 = c.heads * tok;
         a.kv_row0 = (int)base_row(kv, layer, step == PV_STEP_SINK ? 0 : step, streams[i]);
         a.kv_head_stride = kv->ltot;
         a.out_tok0 = tok;
+        list_row0[i] = (int)list_rows;
+        list_rows += (long long)c.heads * ((d.n_queries + kQBlock - 1) / kQBlock);
         tok += d.n_queries;
     }
     if (plan_attention(p, kv->n_sm, kv->wl.n_partials, kv->wl.n_counters) < 0)
@@ -818,8 +1117,504 @@ pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int layer, 
     CUtensorMap tq, to;
     if ((st = q_map(kv, q_rot, (long long)c.heads * tok, &tq))) return st;
     if ((st = out_map(kv, out, tok, &to))) return st;
-    cudaError_t e = launch_attn(tq, kv->tm_k, kv->tm_v, to, p, (cudaStream_t)cuda_stream);
-    if (e != cudaSuccess) return cuda_fail(e, "chunk_attn launch");
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    cudaError_t e;
+    if (!by_block) {
+        e = launch_attn(tq, kv->tm_k, kv->tm_v, to, p, s);
+    } else if (kv->n_pages > 0) {
+        PageTable pages;
+        fill_pages(kv, n_streams, streams, &pages);
+        e = launch_store_blocks(kv, tq, to, p, blocks, keep, list_row0, kb, pages, s);
+    } else {
+        e = launch_store_blocks(kv, tq, to, p, blocks, keep, list_row0, kb, FixedRows{}, s);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+    return PV_OK;
+}
+}  // namespace
+
+extern "C" {
+
+pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                        const void* q_rot, void* out, float* lse, void* cuda_stream) {
+    return store_attn(kv, n_streams, streams, layer, step, q_rot, nullptr, 0, out, lse,
+                      cuda_stream);
+}
+
+pv_status pv_block_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                        const void* q_rot, const int* blocks, int keep, void* out, float* lse,
+                        void* cuda_stream) {
+    if (!blocks) return fail(PV_ERR_INVALID_ARG, "blocks is NULL");
+    if (!aligned(blocks, 4)) return fail(PV_ERR_INVALID_ARG, "blocks must be 4-byte aligned");
+    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    return store_attn(kv, n_streams, streams, layer, step, q_rot, blocks, keep, out, lse,
+                      cuda_stream);
+}
+
+// ---------------------------------------------------------------- pages
+}  // extern "C"
+
+namespace {
+// The regions that page copies move: K, V and, where attached, block means.
+void copy_regions(const pv_kv_s* kv, CopyParams* p) {
+    p->base[0] = (char*)kv->kbase;
+    p->base[1] = (char*)kv->vbase;
+    p->base[2] = (char*)kv->summ;
+    p->seg_bytes[0] = p->seg_bytes[1] = (long long)kv->T * kv->cfg.head_dim * sizeof(bf16);
+    p->seg_bytes[2] = (long long)blocks_per_seg(kv) * kv->cfg.head_dim * sizeof(float);
+    p->n_regions = kv->summ ? 3 : 2;
+    p->heads = kv->cfg.heads;
+    p->head_segs = head_segs(kv);
+    p->planes = kv->cfg.layers * kv->cfg.steps;
+    p->plane_segs = plane_segs(kv);
+}
+}  // namespace
+
+extern "C" {
+
+pv_status pv_kv_fork(pv_kv kv, int src, int n_dst, const int* dst, int copy_current,
+                     void* cuda_stream) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    pv_status st = check_streams(kv, n_dst, dst);
+    if (st) return st;
+    if (src < 0 || src >= kv->cfg.max_streams)
+        return fail(PV_ERR_INVALID_ARG, "stream %d outside 0..%d", src, kv->cfg.max_streams - 1);
+    if (kv->device) {
+        if ((st = check_same_device(kv))) return st;
+        if ((st = check_async("an earlier launch"))) return st;
+    }
+    std::lock_guard<std::mutex> lock(kv->mu);
+    const StreamState& s = kv->streams[src];
+    if (s.phase == PV_PHASE_NEW) return fail(PV_ERR_STATE, "stream %d holds nothing to fork", src);
+    for (int i = 0; i < n_dst; ++i)
+        if (kv->streams[dst[i]].phase != PV_PHASE_NEW)
+            return fail(PV_ERR_STATE, "stream %d is in use: release it first", dst[i]);
+    CopyParams p{};
+    p.fan = 1;
+    p.n = n_dst;
+    int page = 0, n_cur = 0;
+    const bool paged = kv->n_pages > 0;
+    if (paged) {
+        current_pages(kv, s, &page, &n_cur);
+        if (copy_current) {
+            for (int i = 0; i < n_dst; ++i) {
+                const int to = find_pages(kv, n_cur);
+                if (to < 0) {
+                    st = no_pages(kv, n_cur);
+                    for (int j = 0; j < i; ++j) hold_pages(kv, p.dst[j], n_cur, -1);
+                    return st;
+                }
+                hold_pages(kv, to, n_cur, 1);
+                p.dst[i] = to;
+            }
+            p.len = n_cur;
+            p.src[0] = page;
+        }
+    } else {
+        // fixed rows: every key that src holds, one run of frames in each head
+        p.len = kv->cfg.first_frames + s.fill;
+        p.src[0] = src * kv->cfg.heads * head_segs(kv);
+        for (int i = 0; i < n_dst; ++i) p.dst[i] = dst[i] * kv->cfg.heads * head_segs(kv);
+    }
+    if (kv->device && p.len > 0) {
+        copy_regions(kv, &p);
+        const cudaError_t e = launch_copy(p, (cudaStream_t)cuda_stream);
+        if (e != cudaSuccess) {
+            if (paged)
+                for (int i = 0; i < n_dst; ++i) hold_pages(kv, p.dst[i], n_cur, -1);
+            return cuda_fail(e, "fork copy launch");
+        }
+    }
+    for (int i = 0; i < n_dst; ++i) {
+        StreamState& d = kv->streams[dst[i]];
+        d = s;
+        if (!paged) continue;
+        if (d.sink_page >= 0) hold_pages(kv, d.sink_page, kv->cfg.first_frames, 1);
+        for (int r = 0; r < kv->cfg.ring_slots; ++r)
+            if (d.page[r] >= 0) ++kv->ref[d.page[r]];
+        if (!copy_current) continue;
+        // its own copy in place of src's page(s)
+        hold_pages(kv, page, n_cur, -1);
+        (s.phase == PV_PHASE_STEADY ? d.page[s.slot] : d.sink_page) = p.dst[i];
+    }
+    return PV_OK;
+}
+
+pv_status pv_kv_release(pv_kv kv, int stream) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    if (stream < 0 || stream >= kv->cfg.max_streams)
+        return fail(PV_ERR_INVALID_ARG, "stream %d outside 0..%d", stream, kv->cfg.max_streams - 1);
+    std::lock_guard<std::mutex> lock(kv->mu);
+    release_pages(kv, kv->streams[stream]);
+    kv->streams[stream] = StreamState();
+    return PV_OK;
+}
+
+pv_status pv_kv_compact(pv_kv kv, int* moved, void* cuda_stream) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    if (moved) *moved = 0;
+    pv_status st;
+    if (kv->device) {
+        if ((st = check_same_device(kv))) return st;
+        if ((st = check_async("an earlier launch"))) return st;
+    }
+    std::lock_guard<std::mutex> lock(kv->mu);
+    int live = 0, n_moved = 0;
+    CopyParams p{};
+    p.len = 1;
+    if (kv->device) copy_regions(kv, &p);
+    auto flush = [&]() -> cudaError_t {
+        const cudaError_t e =
+            kv->device && p.n > 0 ? launch_copy(p, (cudaStream_t)cuda_stream) : cudaSuccess;
+        p.n = 0;
+        return e;
+    };
+    // held pages slide down in ascending order: a run of consecutive ones
+    // (a sink) stays one
+    for (int i = 0; i < kv->n_pages; ++i) {
+        if (kv->ref[i] == 0) continue;
+        kv->remap[i] = live;
+        if (live != i) {
+            p.src[p.n] = i;
+            p.dst[p.n] = live;
+            ++n_moved;
+            if (++p.n == kMaxMoves) {
+                const cudaError_t e = flush();
+                if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
+            }
+        }
+        ++live;
+    }
+    const cudaError_t e = flush();
+    if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
+    for (int i = 0; i < kv->n_pages; ++i)
+        if (kv->ref[i] > 0 && kv->remap[i] != i) {
+            kv->ref[kv->remap[i]] = kv->ref[i];
+            kv->ref[i] = 0;
+        }
+    for (StreamState& s : kv->streams) {
+        if (s.sink_page >= 0) s.sink_page = kv->remap[s.sink_page];
+        for (int r = 0; r < kv->cfg.ring_slots; ++r)
+            if (s.page[r] >= 0) s.page[r] = kv->remap[s.page[r]];
+    }
+    if (moved) *moved = n_moved;
+    return PV_OK;
+}
+
+pv_status pv_kv_page_table(pv_kv kv, int stream, int* sink_page, int* pages) {
+    if (!kv || !sink_page || !pages) return fail(PV_ERR_INVALID_ARG, "NULL argument");
+    if (stream < 0 || stream >= kv->cfg.max_streams)
+        return fail(PV_ERR_INVALID_ARG, "stream %d outside 0..%d", stream, kv->cfg.max_streams - 1);
+    if (kv->n_pages == 0) return fail(PV_ERR_STATE, "the store has fixed rows, no pages");
+    std::lock_guard<std::mutex> lock(kv->mu);
+    const StreamState& s = kv->streams[stream];
+    *sink_page = s.sink_page;
+    for (int i = 0; i < PV_MAX_RING; ++i) pages[i] = i < kv->cfg.ring_slots ? s.page[i] : -1;
+    return PV_OK;
+}
+
+pv_status pv_kv_free_pages(pv_kv kv, int* n_free, int* longest_run) {
+    if (!kv || !n_free || !longest_run) return fail(PV_ERR_INVALID_ARG, "NULL argument");
+    std::lock_guard<std::mutex> lock(kv->mu);
+    int run = 0;
+    *n_free = *longest_run = 0;
+    for (int r : kv->ref) {
+        run = r == 0 ? run + 1 : 0;
+        *n_free += r == 0;
+        *longest_run = std::max(*longest_run, run);
+    }
+    return PV_OK;
+}
+
+// ---------------------------------------------------------------- key blocks
+pv_status pv_kv_summary_bytes(pv_kv kv, size_t* bytes) {
+    if (!kv || !bytes) return fail(PV_ERR_INVALID_ARG, "NULL argument");
+    *bytes = (size_t)(region_rows(kv) / kv->T) * blocks_per_seg(kv) * kv->cfg.head_dim * sizeof(float);
+    return PV_OK;
+}
+
+pv_status pv_kv_set_summaries(pv_kv kv, void* summ_dev, size_t bytes) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    if (!kv->device) return fail(PV_ERR_STATE, "bookkeeping-only handle has no device buffers");
+    size_t need = 0;
+    pv_status st = pv_kv_summary_bytes(kv, &need);
+    if (st) return st;
+    if (summ_dev) {
+        if (bytes < need)
+            return fail(PV_ERR_CAPACITY, "block means of %zu bytes, need %zu", bytes, need);
+        if (!aligned(summ_dev, 256))
+            return fail(PV_ERR_INVALID_ARG, "block means must be 256-byte aligned");
+        if ((st = check_same_device(kv))) return st;
+        const cudaError_t e = cudaMemset(summ_dev, 0, need);
+        if (e != cudaSuccess) return cuda_fail(e, "clearing the block means");
+    }
+    std::lock_guard<std::mutex> lock(kv->mu);
+    kv->summ = (float*)summ_dev;
+    return PV_OK;
+}
+
+pv_status pv_block_summarize(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                             void* cuda_stream) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    if (!kv->device) return fail(PV_ERR_STATE, "bookkeeping-only handle has no device buffers");
+    pv_status st = check_read(kv, n_streams, streams, layer, step);
+    if (st) return st;
+    if ((st = check_same_device(kv))) return st;
+    if ((st = check_async("an earlier launch"))) return st;
+    std::lock_guard<std::mutex> lock(kv->mu);
+    if (!kv->summ) return fail(PV_ERR_STATE, "no block means attached (pv_kv_set_summaries)");
+    const pv_kv_config& c = kv->cfg;
+    SummaryParams p{};
+    p.k = kv->kbase;
+    p.means = kv->summ;
+    p.head_dim = c.head_dim;
+    p.heads = c.heads;
+    p.seg_len = kv->T;
+    p.bps = blocks_per_seg(kv);
+    p.head_segs = head_segs(kv);
+    p.planes = step == PV_STEP_SINK ? c.steps : 1;
+    p.plane_segs = plane_segs(kv);
+    p.n_runs = n_streams;
+    long long items = 0;
+    for (int i = 0; i < n_streams; ++i) {
+        const StreamState& s = kv->streams[streams[i]];
+        if ((st = check_read_phase(s, streams[i], step))) return st;
+        if ((st = check_owned(kv, s, streams[i]))) return st;
+        const bool steady = s.phase == PV_PHASE_STEADY;
+        p.n_segs[i] = steady ? 1 : c.first_frames;
+        p.seg0[i] = (int)(base_row(kv, layer, std::max(step, 0), streams[i]) / kv->T) +
+                    page_of(kv, s, steady ? c.first_frames + s.slot : 0);
+        p.item0[i] = (int)items;
+        items += (long long)p.n_segs[i] * p.bps;
+        if (items >= (1LL << 31)) return fail(PV_ERR_SHAPE, "too many blocks in one call");
+    }
+    if (c.heads > 65535) return fail(PV_ERR_SHAPE, "more than 65535 heads");
+    p.n_items = (int)items;
+    const cudaError_t e = launch_summary(p, (cudaStream_t)cuda_stream);
+    if (e != cudaSuccess) return cuda_fail(e, "block means launch");
+    return PV_OK;
+}
+
+pv_status pv_block_select(pv_kv kv, int n_streams, const int* streams, int layer, int step,
+                          const void* q_rot, int keep, int force, int* blocks, void* cuda_stream) {
+    if (!kv) return fail(PV_ERR_INVALID_ARG, "handle is NULL");
+    if (!kv->device) return fail(PV_ERR_STATE, "bookkeeping-only handle has no device buffers");
+    pv_status st = check_read(kv, n_streams, streams, layer, step);
+    if (st) return st;
+    if (!q_rot || !blocks) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!aligned(q_rot, 16) || !aligned(blocks, 4))
+        return fail(PV_ERR_INVALID_ARG, "q_rot must be 16-byte, blocks 4-byte aligned");
+    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if (force & ~(PV_FORCE_SINK | PV_FORCE_CURRENT))
+        return fail(PV_ERR_INVALID_ARG, "force %d has unknown bits", force);
+    if ((st = check_same_device(kv))) return st;
+    if ((st = check_async("an earlier launch"))) return st;
+    std::lock_guard<std::mutex> lock(kv->mu);
+    if (!kv->summ) return fail(PV_ERR_STATE, "no block means attached (pv_kv_set_summaries)");
+    const pv_kv_config& c = kv->cfg;
+    SelectParams p{};
+    p.q = (const bf16*)q_rot;
+    p.means = kv->summ;
+    p.blocks = blocks;
+    p.head_dim = c.head_dim;
+    p.heads = c.heads;
+    p.keep = keep;
+    p.n_streams = n_streams;
+    for (int i = 0; i < n_streams; ++i)
+        if ((st = check_read_phase(kv->streams[streams[i]], streams[i], step))) return st;
+    if ((st = store_blocks(kv, n_streams, streams, layer, step, &p.kb))) return st;
+    long long items = 0, rows = 0;
+    for (int i = 0; i < n_streams; ++i) {
+        const StreamState& s = kv->streams[streams[i]];
+        pv_kv_state d;
+        derive(kv, s, &d);
+        if (p.kb.n_blocks[i] > kMaxSelectBlocks)
+            return fail(PV_ERR_SHAPE, "stream %d: %d blocks, the selection holds %d", streams[i],
+                        p.kb.n_blocks[i], kMaxSelectBlocks);
+        int forced = 0;
+        if (s.phase == PV_PHASE_STEADY) {
+            if (force & PV_FORCE_SINK) {
+                p.force1[i][0] = c.first_frames * p.kb.bps;
+                forced += p.force1[i][0];
+            }
+            if (force & PV_FORCE_CURRENT) {
+                p.force0[i][1] = (c.first_frames + s.slot) * p.kb.bps;
+                p.force1[i][1] = p.force0[i][1] + p.kb.bps;
+                forced += p.kb.bps;
+            }
+        }
+        if (forced > keep)
+            return fail(PV_ERR_SHAPE, "stream %d: %d forced blocks, keep %d", streams[i], forced, keep);
+        p.n_q[i] = d.n_queries;
+        p.q_row0[i] = rows;
+        p.item0[i] = (int)items;
+        p.max_blocks = std::max(p.max_blocks, p.kb.n_blocks[i]);
+        rows += (long long)c.heads * d.n_queries;
+        items += (long long)c.heads * ((d.n_queries + kQBlock - 1) / kQBlock);
+    }
+    if (items > (1 << 27)) return fail(PV_ERR_SHAPE, "too many query groups");
+    p.n_items = (int)items;
+    PageTable pages;
+    if (kv->n_pages > 0) fill_pages(kv, n_streams, streams, &pages);
+    const cudaError_t e =
+        launch_select(p, kv->n_pages > 0 ? &pages : nullptr, (cudaStream_t)cuda_stream);
+    if (e != cudaSuccess) return cuda_fail(e, "block selection launch");
+    return PV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+// Shape checks of the explicit-buffer block calls; *nb: blocks of n_k keys.
+pv_status dense_blocks(int n_q, int n_k, int heads, int head_dim, int* nb) {
+    if (n_q < 1 || n_k < 1 || heads < 1 || (head_dim != 64 && head_dim != 128))
+        return fail(PV_ERR_SHAPE, "n_q, n_k, heads must be positive and head_dim 64 or 128");
+    if (n_q > kMaxLen || n_k > kMaxLen)
+        return fail(PV_ERR_SHAPE, "n_q %d or n_k %d above %d", n_q, n_k, kMaxLen);
+    if ((long long)n_q * heads >= (1LL << 31) || (long long)n_k * heads >= (1LL << 31))
+        return fail(PV_ERR_SHAPE, "heads * n_q or heads * n_k is 2^31 or more");
+    *nb = (n_k + kKeyTile - 1) / kKeyTile;
+    return PV_OK;
+}
+KeyBlocks one_segment(int n_k, int nb) {
+    KeyBlocks kb{};
+    kb.seg_len = n_k;
+    kb.bps = nb;
+    kb.tail = n_k - (nb - 1) * kKeyTile;
+    kb.head_segs = 1;
+    kb.n_blocks[0] = nb;
+    return kb;
+}
+}  // namespace
+
+extern "C" {
+
+pv_status pv_block_summarize_dense(const void* k, int n_k, int heads, int head_dim, float* means,
+                                   void* cuda_stream) {
+    int nb = 0;
+    pv_status st = dense_blocks(1, n_k, heads, head_dim, &nb);
+    if (st) return st;
+    if (heads > 65535) return fail(PV_ERR_SHAPE, "more than 65535 heads");
+    if (!k || !means) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!aligned(k, 16) || !aligned(means, 16))
+        return fail(PV_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    if ((st = check_async("an earlier launch"))) return st;
+    if ((st = check_device(nullptr))) return st;
+    SummaryParams p{};
+    p.k = (const bf16*)k;
+    p.means = means;
+    p.head_dim = head_dim;
+    p.heads = heads;
+    p.seg_len = n_k;
+    p.bps = nb;
+    p.head_segs = 1;
+    p.planes = 1;
+    p.n_runs = 1;
+    p.n_segs[0] = 1;
+    p.n_items = nb;
+    const cudaError_t e = launch_summary(p, (cudaStream_t)cuda_stream);
+    if (e != cudaSuccess) return cuda_fail(e, "block means launch");
+    return PV_OK;
+}
+
+pv_status pv_block_select_dense(const void* q, const float* means, int n_q, int n_k, int heads,
+                                int head_dim, int keep, int n_front, int* blocks,
+                                void* cuda_stream) {
+    int nb = 0;
+    pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
+    if (st) return st;
+    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if (n_front < 0 || n_front > keep)
+        return fail(PV_ERR_SHAPE, "n_front %d outside 0..keep = %d", n_front, keep);
+    if (nb > kMaxSelectBlocks)
+        return fail(PV_ERR_SHAPE, "%d blocks, the selection holds %d", nb, kMaxSelectBlocks);
+    const long long groups = (n_q + kQBlock - 1) / kQBlock;
+    if (heads * groups > (1 << 27)) return fail(PV_ERR_SHAPE, "too many query groups");
+    if (!q || !means || !blocks) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!aligned(q, 16) || !aligned(means, 16) || !aligned(blocks, 4))
+        return fail(PV_ERR_INVALID_ARG, "q and means must be 16-byte, blocks 4-byte aligned");
+    if ((st = check_async("an earlier launch"))) return st;
+    if ((st = check_device(nullptr))) return st;
+    SelectParams p{};
+    p.q = (const bf16*)q;
+    p.means = means;
+    p.blocks = blocks;
+    p.head_dim = head_dim;
+    p.heads = heads;
+    p.keep = keep;
+    p.n_streams = 1;
+    p.n_items = (int)(heads * groups);
+    p.max_blocks = nb;
+    p.n_q[0] = n_q;
+    p.force1[0][0] = n_front;
+    p.kb = one_segment(n_k, nb);
+    const cudaError_t e = launch_select(p, nullptr, (cudaStream_t)cuda_stream);
+    if (e != cudaSuccess) return cuda_fail(e, "block selection launch");
+    return PV_OK;
+}
+
+pv_status pv_block_attn_dense_ws_bytes(int n_q, int n_k, int heads, int head_dim, int keep,
+                                       size_t* ws_bytes) {
+    int nb = 0;
+    pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
+    if (st) return st;
+    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    return pv_attn_dense_ws_bytes(n_q, std::min(keep, nb) * kKeyTile, heads, head_dim, ws_bytes);
+}
+
+pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n_q, int n_k,
+                              int heads, int head_dim, const int* blocks, int keep, void* out,
+                              float* lse, void* ws, size_t ws_bytes, void* cuda_stream) {
+    if (!q || !k || !v || !out || !blocks) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
+    int nb = 0;
+    pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
+    if (st) return st;
+    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+        (lse && !aligned(lse, 4)) || !aligned(blocks, 4))
+        return fail(PV_ERR_INVALID_ARG, "tensors must be 16-byte aligned, lse and blocks 4-byte");
+    const int n_sel = std::min(keep, nb);
+    size_t need = 0;
+    if ((st = pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep, &need))) return st;
+    if (!ws || ws_bytes < need || !aligned(ws, 256))
+        return fail(PV_ERR_CAPACITY, "workspace of %zu bytes at %p, need %zu (256-byte aligned)",
+                    ws_bytes, ws, need);
+    if ((st = check_async("an earlier launch"))) return st;
+    int n_sm = 148;
+    if ((st = check_device(&n_sm))) return st;
+    const size_t n_qb = (n_q + kQBlock - 1) / kQBlock;
+    const size_t cnt = (size_t)heads * n_qb * kQTilesPerCta;
+    if (cnt >= (1ull << 31)) return fail(PV_ERR_SHAPE, "too many query groups");
+    const int n_cnt = (int)cnt;
+    const size_t tiles = (size_t)heads * n_qb * n_sel;
+    const int n_part = (int)(4 * std::min<size_t>(kMaxGrid, tiles));
+    AttnParams p{};
+    p.out = (bf16*)out;
+    p.lse = lse;
+    p.err = (int*)ws;
+    p.counters = (int*)((char*)ws + 256);
+    p.partial = (float*)((char*)ws + 256 + round_up((size_t)n_cnt * sizeof(int), 256));
+    p.heads = heads;
+    p.head_dim = head_dim;
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
+    p.n_streams = 1;
+    p.st[0].n_q = n_q;
+    p.st[0].n_k = n_sel * kKeyTile;
+    if (plan_attention(p, n_sm, n_part, n_cnt) < 0)
+        return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
+    BlockArgs<FixedRows> b{};
+    b.list = blocks;
+    b.keep = keep;
+    b.kb = one_segment(n_k, nb);
+    CUtensorMap tq, tk, tv, to;
+    char msg[256];
+    if (!encode_rows_map(&tq, q, (long long)heads * n_q, head_dim, msg, sizeof msg) ||
+        !encode_seg_map(&tk, k, n_k, heads, head_dim, msg, sizeof msg) ||
+        !encode_seg_map(&tv, v, n_k, heads, head_dim, msg, sizeof msg) ||
+        !encode_out_map(&to, out, n_q, heads, head_dim, msg, sizeof msg))
+        return fail(PV_ERR_CUDA, "%s", msg);
+    const cudaError_t e = launch_block_attn(tq, tk, tv, to, p, b, (cudaStream_t)cuda_stream);
+    if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
     return PV_OK;
 }
 

@@ -31,6 +31,8 @@
 // Every mbarrier wait is bounded (about one second); a wait that gives up
 // sets the device error word, makes the CTA skip its remaining work, waits
 // (bounded) for its own copies and MMAs, frees TMEM and returns.
+#include <type_traits>
+
 #include "pv_internal.h"
 
 namespace pv {
@@ -129,6 +131,15 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -373,10 +384,41 @@ __device__ __forceinline__ size_t part_slot(const AttnParams& p, int c, long lon
     return ((size_t)c * 2 + which) * 2 + X;
 }
 
+// Listed blocks (BlockArgs): block of the segment's key tile j, or -1 past its
+// last tile; entries outside the sequence count as empty blocks.
+template <typename B>
+struct BlockRow {
+    const int* row;
+    int n, n_blocks, kt0;
+    __device__ BlockRow(const B& ba, const AttnParams& p, const Seg& g) {
+        const AttnStreamDesc& s = p.st[g.si];
+        n = g.n;
+        kt0 = g.kt0;
+        n_blocks = ba.kb.n_blocks[s.id];
+        row = ba.list ? ba.list + (ba.list_row0[s.id] + (long long)g.head * s.n_qb + g.qb) * ba.keep + kt0
+                      : nullptr;
+    }
+    __device__ int at(int j) const {
+        if (j >= n) return -1;
+        const int b = row ? __ldg(row + j) : kt0 + j;
+        return (unsigned)b < (unsigned)n_blocks ? b : -1;
+    }
+};
+struct NoRow {
+    __device__ NoRow(const NoBlocks&, const AttnParams&, const Seg&) {}
+};
+template <typename B>
+using BlockRowOf = std::conditional_t<B::kBlocks, BlockRow<B>, NoRow>;
+// Keys of block b: 128, fewer in the last block of a segment, 0 if empty.
+__device__ __forceinline__ int block_keys(const KeyBlocks& k, int b) {
+    if (b < 0) return 0;
+    return (b + 1) % k.bps == 0 ? k.tail : kKeyTile;
+}
+
 // ----------------------------------------------------------------- roles
-template <int D, bool kRun>
+template <int D, bool kRun, typename B>
 __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                         const AttnParams& p, uint8_t* smem, Bars* b) {
+                         const AttnParams& p, const B& ba, uint8_t* smem, Bars* b) {
     using C = Cfg<D>;
     const uint32_t qbar = smem_u32(&b->q_full);
     int kv = 0, qseg = 0;
@@ -398,8 +440,24 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUt
                 tma_load(smem_u32(smem + C::kQOff + t * C::kTileBytes + c * 16384), tq, c * 64,
                          qrow + t * kQRows, qbar);
         ++qseg;
-        const int krow0 = s.kv_row0 + g.head * s.kv_head_stride + g.kt0 * kKeyTile;
+        int krow0 = 0;                 // contiguous keys: row of the next tile
+        int next_b = 0;                // listed blocks: the next tile's block,
+        int brow = 0, bseg = 0;        // and where the current one lies
+        const BlockRowOf<B> br(ba, p, g);
+        if constexpr (B::kBlocks)
+            next_b = br.at(0);
+        else
+            krow0 = s.kv_row0 + g.head * s.kv_head_stride + g.kt0 * kKeyTile;
         for (int j = 0; ok && j < g.n; ++j) {
+            if constexpr (B::kBlocks) {
+                const int blk = max(next_b, 0);
+                const bool empty = next_b < 0;
+                next_b = br.at(j + 1);  // one tile ahead of its use
+                const int seg = blk / ba.kb.bps;
+                // an empty block lies past its segment's end: it reads as zeros
+                brow = (empty ? ba.kb.bps : blk - seg * ba.kb.bps) * kKeyTile;
+                bseg = ba.kb.seg0[s.id] + g.head * ba.kb.head_segs + ba.pages.page(ba.kb, s.id, seg);
+            }
             for (int w = 0; w < 2; ++w) {
                 const int st = kv % C::kStages;
                 // the tile loaded kStages loads ago must have been released
@@ -413,9 +471,13 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUt
                 const uint32_t full = smem_u32(&b->kv_full[st]);
                 mbar_expect_tx(full, C::kTileBytes);
                 const CUtensorMap* m = w == 0 ? tk : tv;
-                for (int c = 0; c < C::kSub; ++c)
-                    tma_load(smem_u32(smem + C::kKVOff + st * C::kTileBytes + c * 16384), m,
-                             c * 64, krow0 + j * kKeyTile, full);
+                for (int c = 0; c < C::kSub; ++c) {
+                    const uint32_t dst = smem_u32(smem + C::kKVOff + st * C::kTileBytes + c * 16384);
+                    if constexpr (B::kBlocks)
+                        tma_load_3d(dst, m, c * 64, brow, bseg, full);
+                    else
+                        tma_load(dst, m, c * 64, krow0 + j * kKeyTile, full);
+                }
                 ++kv;
             }
         }
@@ -569,6 +631,28 @@ __device__ __forceinline__ float exp_half(const uint32_t* sr, float2 sl2x2, floa
     return a.x + a.y;
 }
 
+// The same for listed blocks, with P rounded to nearest (half an ulp of the
+// last kept bit added before the byte permute; the same instruction count as
+// the truncation above) and the sum taken over the unrounded f32 values: the
+// rounding errors of P then average out in O, and the log-sum-exp keeps f32
+// accuracy.
+__device__ __forceinline__ float exp_half_rn(const uint32_t* sr, float2 sl2x2, float2 nmx2,
+                                             uint32_t tP) {
+    float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    uint32_t pk[32];
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
+                                    sl2x2, nmx2);
+        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+        acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], e);
+        pk[i / 2] = __byte_perm(__float_as_uint(e.x) + 0x8000u, __float_as_uint(e.y) + 0x8000u, 0x7632);
+    }
+    tmem_st32(tP, pk);
+    const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+    return a.x + a.y;
+}
+
 // Row maximum of 128 scores (masked ones are -inf).
 __device__ __forceinline__ float row_max(const uint32_t* sr) {
     float mx8[8];
@@ -664,7 +748,7 @@ __device__ __forceinline__ void l2_discard(const float* a, float after) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(a), "f"(after) : "memory");
 }
 
-template <int D>
+template <int D, bool kBlocks>
 __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, int X, int r,
                                             bool row_ok, bool keep, uint32_t tO, float m_own,
                                             float l_own, bf16* dst, float* lse_dst,
@@ -695,7 +779,9 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, i
             }
         }
     }
-    const float invL = 1.0f / L;
+    // listed blocks may leave a row without keys: it gives 0 and -inf
+    const bool none = kBlocks && !(L > 0.f);
+    const float invL = none ? 0.f : 1.0f / L;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         float acc[32];
@@ -728,7 +814,8 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, i
             store_row32(dst + c, o, 1.0f);
         }
     }
-    if (row_ok && lse_dst) *lse_dst = (M + __log2f(L)) * 0.69314718055994531f;
+    if (row_ok && lse_dst)
+        *lse_dst = none ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
     // every part's lines of this warp's 32 rows (the merging CTA's own part
     // too: it was written before the arrival count and read from TMEM): a
     // line per lane and 32 columns, then the m and l lines
@@ -740,9 +827,14 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, i
     }
 }
 
-template <int D, bool kRun>
-__device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uint8_t* smem,
-                                 Bars* b, uint32_t tmem, int X) {
+// Lower bound of the running maximum over listed blocks: an all-masked tile
+// leaves it there, its exponentials are 2^(-inf) = 0, and the next tile with
+// a key moves it up.
+constexpr float kEmptyMax = -3.0e38f;
+
+template <int D, bool kRun, typename B>
+__device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtensorMap* to,
+                                 uint8_t* smem, Bars* b, uint32_t tmem, int X) {
     using C = Cfg<D>;
     const int wq = (threadIdx.x / 32) & 3;          // TMEM lane quadrant of this warp
     const int r = wq * 32 + (threadIdx.x & 31);     // query row inside the tile
@@ -764,15 +856,24 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
         if (g.rows[X] == 0) continue;  // this segment has no query tile X
         const AttnStreamDesc& s = p.st[g.si];
         float m = -INFINITY;  // maximum applied to the exponentials, log2 units
-        float l = 0.f;        // sum of the exponentials (as rounded into P)
+        float l = 0.f;        // sum of the exponentials (contiguous keys: as rounded into P)
+        const BlockRowOf<B> br(ba, p, g);
+        int next_b = 0;       // listed blocks: the next tile's block
+        if constexpr (B::kBlocks) next_b = br.at(0);
         for (int j = 0; j < g.n; ++j) {
+            int valid;
+            if constexpr (B::kBlocks) {
+                valid = block_keys(ba.kb, next_b);
+                next_b = br.at(j + 1);
+            } else {
+                valid = s.n_k - (g.kt0 + j) * kKeyTile;
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&b->s_full[X]), sc & 1, b, p.err));
             if (!ok) break;
             ++sc;
             tc_fence_after();
             uint32_t sr[128];
             tmem_ld128_wait(tS, sr);
-            const int valid = s.n_k - (g.kt0 + j) * kKeyTile;
             if (valid < kKeyTile) {
 #pragma unroll
                 for (int c = 0; c < 128; ++c)
@@ -783,7 +884,7 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
                 // more than 8 (log2 units), so p stays <= 2^8
                 const float m_t = row_max(sr) * sl2;
                 if (j == 0) {
-                    m = m_t;
+                    m = B::kBlocks ? fmaxf(m_t, kEmptyMax) : m_t;
                 } else if (__any_sync(0xffffffffu, m_t > m + 8.0f)) {
                     const float m_new = fmaxf(m, m_t);
                     const float alpha = ex2(m - m_new);
@@ -805,12 +906,18 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
             // 0..63) while the second half's exponentials are computed
             const float2 sl2x2 = make_float2(sl2, sl2);
             const float2 nmx2 = make_float2(-m, -m);
-            l += exp_half(sr, sl2x2, nmx2, tS);
+            if constexpr (B::kBlocks)
+                l += exp_half_rn(sr, sl2x2, nmx2, tS);
+            else
+                l += exp_half(sr, sl2x2, nmx2, tS);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&b->p_lo[X]));
-            l += exp_half(sr + 64, sl2x2, nmx2, tS + 32);
+            if constexpr (B::kBlocks)
+                l += exp_half_rn(sr + 64, sl2x2, nmx2, tS + 32);
+            else
+                l += exp_half(sr + 64, sl2x2, nmx2, tS + 32);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -829,7 +936,8 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
         // count says whether this CTA merges: the merge then reads its own
         // part from there instead of back from global memory.
         const bool keep = !whole && it.pos >= it.end;
-        const float inv = 1.0f / l;
+        const bool none = B::kBlocks && !(l > 0.f);  // a row without keys: 0 and -inf
+        const float inv = none ? 0.f : 1.0f / l;
         bf16* dst = p.out + ((size_t)tok * p.heads + g.head) * D;
         float* mine = p.partial + part_slot(p, blockIdx.x, g.i0, X) * slot_f;
         const bool warp_full = wq * 32 + 31 < g.rows[X];  // all 32 rows of this warp are queries
@@ -864,7 +972,8 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
             if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&b->o_empty[X]));
         }
         if (whole) {
-            if (row_ok && p.lse) p.lse[(size_t)tok * p.heads + g.head] = (m + __log2f(l)) * ln2;
+            if (row_ok && p.lse)
+                p.lse[(size_t)tok * p.heads + g.head] = none ? -INFINITY : (m + __log2f(l)) * ln2;
             continue;
         }
         {
@@ -894,7 +1003,7 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
         ++ec;
         if (ok && b->last[X]) {
             fence_gpu();
-            merge_parts<D>(p, g, X, r, row_ok, keep, tO, m, l, dst,
+            merge_parts<D, B::kBlocks>(p, g, X, r, row_ok, keep, tO, m, l, dst,
                            p.lse ? p.lse + (size_t)tok * p.heads + g.head : nullptr, to, ebuf,
                            warp_full, tok_w);
         }
@@ -910,12 +1019,14 @@ __device__ void softmax_epilogue(const AttnParams& p, const CUtensorMap* to, uin
 }
 
 // kRun: whole items handed out at run time (AttnParams::item_aligned == 1);
-// otherwise stream-K.  Two instantiations, so that each keeps its own code.
-template <int D, bool kRun>
+// otherwise stream-K.  B: NoBlocks for contiguous keys, BlockArgs for listed
+// blocks in fixed rows or pages.  Instantiations, so that each keeps its own
+// code.
+template <int D, bool kRun, typename B>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-                const __grid_constant__ AttnParams p) {
+                const __grid_constant__ AttnParams p, const __grid_constant__ B ba) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -961,13 +1072,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp == 0) {
-            if (lane_id == 0) producer<D, kRun>(&tq, &tk, &tv, p, smem, b);
+            if (lane_id == 0) producer<D, kRun>(&tq, &tk, &tv, p, ba, smem, b);
         } else if (warp == 1) {
             mma_issuer<D, kRun>(p, smem, b, tmem);  // the whole warp; one elected lane issues
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-        softmax_epilogue<D, kRun>(p, &to, smem, b, tmem, warp / 4 - 1);
+        softmax_epilogue<D, kRun>(p, ba, &to, smem, b, tmem, warp / 4 - 1);
     }
     tc_fence_before();
     __syncthreads();
@@ -987,15 +1098,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool kRun>
+template <int D, bool kRun, typename B>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                     const CUtensorMap& to, const AttnParams& p, cudaStream_t s) {
+                     const CUtensorMap& to, const AttnParams& p, const B& ba, cudaStream_t s) {
     using C = Cfg<D>;
     static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(attn_kernel<D, kRun>, C::kSmem, configured);
+    const cudaError_t e = smem_limit_once(attn_kernel<D, kRun, B>, C::kSmem, configured);
     if (e != cudaSuccess) return e;
-    attn_kernel<D, kRun><<<p.grid, kThreads, C::kSmem, s>>>(tq, tk, tv, to, p);
+    attn_kernel<D, kRun, B><<<p.grid, kThreads, C::kSmem, s>>>(tq, tk, tv, to, p, ba);
     return cudaGetLastError();
+}
+
+template <typename B>
+cudaError_t launch_any(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const CUtensorMap& to, const AttnParams& p, const B& ba, cudaStream_t s) {
+    if (p.grid <= 0 || p.total <= 0) return cudaErrorInvalidValue;
+    const bool run = p.item_aligned != 0;
+    if (p.head_dim == 128)
+        return run ? launch_d<128, true>(tq, tk, tv, to, p, ba, s)
+                   : launch_d<128, false>(tq, tk, tv, to, p, ba, s);
+    if (p.head_dim == 64)
+        return run ? launch_d<64, true>(tq, tk, tv, to, p, ba, s)
+                   : launch_d<64, false>(tq, tk, tv, to, p, ba, s);
+    return cudaErrorInvalidValue;
 }
 
 // One bounded wait on an mbarrier that nothing arrives on: it gives up after
@@ -1020,16 +1145,23 @@ cudaError_t launch_wait_timeout_probe(int* err, cudaStream_t s) {
 
 static_assert(sizeof(AttnParams) + 4 * sizeof(CUtensorMap) <= 4096,
               "attention kernel parameters beyond 4 KB");
+// kernel parameters end at 32,764 bytes
+static_assert(sizeof(AttnParams) + 4 * sizeof(CUtensorMap) + sizeof(BlockArgs<PageTable>) <= 32000,
+              "paged attention kernel parameters too large");
 
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& to, const AttnParams& p, cudaStream_t s) {
-    if (p.grid <= 0 || p.total <= 0) return cudaErrorInvalidValue;
-    const bool run = p.item_aligned != 0;
-    if (p.head_dim == 128)
-        return run ? launch_d<128, true>(tq, tk, tv, to, p, s) : launch_d<128, false>(tq, tk, tv, to, p, s);
-    if (p.head_dim == 64)
-        return run ? launch_d<64, true>(tq, tk, tv, to, p, s) : launch_d<64, false>(tq, tk, tv, to, p, s);
-    return cudaErrorInvalidValue;
+    return launch_any(tq, tk, tv, to, p, NoBlocks{}, s);
+}
+cudaError_t launch_block_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& to, const AttnParams& p,
+                              const BlockArgs<FixedRows>& b, cudaStream_t s) {
+    return launch_any(tq, tk, tv, to, p, b, s);
+}
+cudaError_t launch_block_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& to, const AttnParams& p,
+                              const BlockArgs<PageTable>& b, cudaStream_t s) {
+    return launch_any(tq, tk, tv, to, p, b, s);
 }
 
 }  // namespace pv

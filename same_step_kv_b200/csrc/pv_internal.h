@@ -70,6 +70,7 @@ struct AttnStreamDesc {
     int n_qb;            // query blocks of kQBlock rows
     int n_kt;            // key tiles
     int item0;           // global index of this stream's first (head, query block) item
+    int id;              // position in the caller's list (the planner may reorder streams)
     long long cost0;     // key tiles of all items before this stream's first
 };
 
@@ -101,6 +102,116 @@ __host__ __device__ inline size_t partial_slot_floats(int D) { return (size_t)kQ
 
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& to, const AttnParams& p, cudaStream_t s);
+
+// ------------------------------------------------- key blocks and pages
+// Keys of a (plane, head) lie in segments of seg_len rows: the latent frames
+// of a store (seg_len = T), or the one segment of an explicit buffer.  A
+// segment holds bps = ceil(seg_len / 128) blocks of 128 keys, the last one
+// with `tail` keys.  Block b of a sequence is block b % bps of its segment
+// b / bps.  Where segment s lies in memory is its physical segment
+// seg0 + head * head_segs + page(s): page(s) = s in fixed rows, the stream's
+// page table in a paged store.
+struct KeyBlocks {
+    int seg_len, bps, tail;
+    int head_segs;       // physical segments between heads
+    int first;           // segments of the sink run (paged store)
+    int seg0[PV_MAX_STREAMS];      // physical segment of head 0, page 0
+    int n_blocks[PV_MAX_STREAMS];
+};
+struct FixedRows {
+    __host__ __device__ static int page(const KeyBlocks&, int, int seg) { return seg; }
+};
+// Pages of the listed streams: the sink's first page (its pages are
+// consecutive), then one page per ring slot.
+struct PageTable {
+    int sink[PV_MAX_STREAMS];
+    int ring[PV_MAX_STREAMS][PV_MAX_RING];
+    __host__ __device__ int page(const KeyBlocks& k, int stream, int seg) const {
+        return seg < k.first ? sink[stream] + seg : ring[stream][seg - k.first];
+    }
+};
+
+// Attention over listed blocks: every (head, query block) item reads the
+// blocks of its list row, list_row0 + head * n_qb + query block, of `keep`
+// entries; without a list it reads its stream's blocks 0 .. n_kt - 1.
+template <typename Pages>
+struct BlockArgs {
+    static constexpr bool kBlocks = true;
+    const int* list;
+    int keep;
+    int list_row0[PV_MAX_STREAMS];
+    KeyBlocks kb;
+    Pages pages;
+};
+struct NoBlocks {  // contiguous keys
+    static constexpr bool kBlocks = false;
+};
+
+// tk, tv: 3D maps (D, seg_len, segments) of encode_seg_map; n_kt of a stream
+// is the number of listed blocks.
+cudaError_t launch_block_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& to, const AttnParams& p,
+                              const BlockArgs<FixedRows>& b, cudaStream_t s);
+cudaError_t launch_block_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& to, const AttnParams& p,
+                              const BlockArgs<PageTable>& b, cudaStream_t s);
+// K or V rows as segments: a box is 128 rows x 64 columns of one segment,
+// and rows past the segment's end read as zeros.
+bool encode_seg_map(CUtensorMap* map, const void* base, int seg_len, long long segs, int D,
+                    char* err, size_t errlen);
+
+// Means of key blocks (pv_blocks.cu): runs of n_segs[i] physical segments
+// from seg0[i] (head 0), for every head and `planes` planes that lie
+// plane_segs segments apart.
+struct SummaryParams {
+    const bf16* k;
+    float* means;        // f32 [physical segment][bps][D]
+    int head_dim, heads;
+    int seg_len, bps, head_segs;
+    int planes;
+    long long plane_segs;
+    int n_runs;
+    int seg0[PV_MAX_STREAMS];
+    int n_segs[PV_MAX_STREAMS];
+    int item0[PV_MAX_STREAMS];   // blocks of all runs before run i
+    int n_items;                 // blocks of all runs
+};
+cudaError_t launch_summary(const SummaryParams& p, cudaStream_t s);
+
+// Block selection (pv_blocks.cu): one item per (stream, head, query group).
+constexpr int kMaxSelectBlocks = 16384;   // blocks of one sequence
+struct SelectParams {
+    const bf16* q;
+    const float* means;
+    int* blocks;
+    int head_dim, heads, keep;
+    int n_streams;
+    int n_items;
+    int max_blocks;
+    int n_q[PV_MAX_STREAMS];
+    int item0[PV_MAX_STREAMS];            // also the first list row
+    long long q_row0[PV_MAX_STREAMS];     // row of head 0, query 0
+    int force0[PV_MAX_STREAMS][2];        // first forced block of two ranges
+    int force1[PV_MAX_STREAMS][2];        // one past the last
+    KeyBlocks kb;
+};
+cudaError_t launch_select(const SelectParams& p, const PageTable* pages, cudaStream_t s);
+
+// Page copies (pv_blocks.cu): physical segments moved in every plane and head
+// of up to three regions (K, V, block means).  fan: the run of len segments
+// from src[0] goes to each of dst[0..n); otherwise segment src[i] goes to
+// dst[i] in the order given, with dst[i] < src[i] and src ascending.
+constexpr int kMaxMoves = 480;
+struct CopyParams {
+    char* base[3];
+    long long seg_bytes[3];
+    int n_regions;
+    int heads, head_segs, planes;
+    long long plane_segs;
+    int fan, len, n;
+    int src[kMaxMoves], dst[kMaxMoves];
+};
+cudaError_t launch_copy(const CopyParams& p, cudaStream_t s);
 
 // One bounded device wait that runs out (failure-path self-test).
 cudaError_t launch_wait_timeout_probe(int* err, cudaStream_t s);

@@ -29,6 +29,9 @@ PV_ERR_TIMEOUT = 7
 PV_STEP_SINK = -1
 PV_MAX_RING = 64
 PV_MAX_STREAMS = 64
+PV_BLOCK_KEYS = 128
+PV_BLOCK_QUERIES = 256
+PV_FORCE_SINK, PV_FORCE_CURRENT = 1, 2
 PV_PHASE_NEW, PV_PHASE_FIRST, PV_PHASE_BOOT, PV_PHASE_STEADY = 0, 1, 2, 3
 
 
@@ -88,6 +91,24 @@ _SIGS = {
     "pv_qkv_ws_bytes": ([_i, _i, ctypes.POINTER(_sz)], _i),
     "pv_qkv_rope_append": ([_vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp,
                             _vp, _sz, _vp], _i),
+    "pv_kv_paged_required_bytes": ([ctypes.POINTER(pv_kv_config), _i, ctypes.POINTER(_sz),
+                                    ctypes.POINTER(_sz)], _i),
+    "pv_kv_init_paged": ([ctypes.POINTER(_vp), ctypes.POINTER(pv_kv_config), _i, _vp, _sz, _vp,
+                          _sz], _i),
+    "pv_kv_fork": ([_vp, _i, _i, ctypes.POINTER(_i), _i, _vp], _i),
+    "pv_kv_release": ([_vp, _i], _i),
+    "pv_kv_compact": ([_vp, ctypes.POINTER(_i), _vp], _i),
+    "pv_kv_page_table": ([_vp, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)], _i),
+    "pv_kv_free_pages": ([_vp, ctypes.POINTER(_i), ctypes.POINTER(_i)], _i),
+    "pv_kv_summary_bytes": ([_vp, ctypes.POINTER(_sz)], _i),
+    "pv_kv_set_summaries": ([_vp, _vp, _sz], _i),
+    "pv_block_summarize": ([_vp, _i, ctypes.POINTER(_i), _i, _i, _vp], _i),
+    "pv_block_select": ([_vp, _i, ctypes.POINTER(_i), _i, _i, _vp, _i, _i, _vp, _vp], _i),
+    "pv_block_attn": ([_vp, _i, ctypes.POINTER(_i), _i, _i, _vp, _vp, _i, _vp, _vp, _vp], _i),
+    "pv_block_summarize_dense": ([_vp, _i, _i, _i, _vp, _vp], _i),
+    "pv_block_select_dense": ([_vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp], _i),
+    "pv_block_attn_dense_ws_bytes": ([_i, _i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "pv_block_attn_dense": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp], _i),
     "pv_sigma_schedule": ([_i, ctypes.c_double, ctypes.c_double, ctypes.POINTER(ctypes.c_double),
                            ctypes.POINTER(_i)], _i),
     "pv_euler_cfg_step": ([_vp, _vp, _vp, _sz, ctypes.c_float, ctypes.c_float, _vp], _i),
@@ -116,6 +137,13 @@ def _ptr(t) -> int | None:
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _dense(t) -> int | None:
+    """_ptr of a tensor that has to be contiguous."""
+    if t is not None and not isinstance(t, int) and not t.is_contiguous():
+        raise PVError(PV_ERR_INVALID_ARG, "tensors must be contiguous")
+    return _ptr(t)
 
 
 def _stream(s):
@@ -191,6 +219,52 @@ def pv_kv_row_offset(kv, layer, step, stream, head, key) -> tuple[int, int]:
     return a.value, b.value
 
 
+def pv_kv_paged_required_bytes(cfg: pv_kv_config, n_pages: int) -> tuple[int, int]:
+    a, b = _sz(), _sz()
+    _check(lib.pv_kv_paged_required_bytes(ctypes.byref(cfg), n_pages, ctypes.byref(a),
+                                          ctypes.byref(b)))
+    return a.value, b.value
+
+
+def pv_kv_init_paged(cfg: pv_kv_config, n_pages: int, kv_dev=None, kv_bytes=0, ws_dev=None,
+                     ws_bytes=0) -> int:
+    h = _vp()
+    _check(lib.pv_kv_init_paged(ctypes.byref(h), ctypes.byref(cfg), n_pages, _ptr(kv_dev), kv_bytes,
+                                _ptr(ws_dev), ws_bytes))
+    return h.value
+
+
+def pv_kv_fork(kv, src: int, dst, copy_current, cuda_stream=None) -> None:
+    """dst: the streams that become branches of src."""
+    n, arr = _streams(dst)
+    _check(lib.pv_kv_fork(kv, src, n, arr, 1 if copy_current else 0, _stream(cuda_stream)))
+
+
+def pv_kv_release(kv, stream: int) -> None:
+    _check(lib.pv_kv_release(kv, stream))
+
+
+def pv_kv_compact(kv, cuda_stream=None) -> int:
+    """The number of pages moved."""
+    n = _i()
+    _check(lib.pv_kv_compact(kv, ctypes.byref(n), _stream(cuda_stream)))
+    return n.value
+
+
+def pv_kv_page_table(kv, stream: int) -> tuple[int, list[int]]:
+    """(first page of the sink, page of each ring slot up to PV_MAX_RING; -1: none)."""
+    sink, pages = _i(), (_i * PV_MAX_RING)()
+    _check(lib.pv_kv_page_table(kv, stream, ctypes.byref(sink), pages))
+    return sink.value, list(pages)
+
+
+def pv_kv_free_pages(kv) -> tuple[int, int]:
+    """(free pages, longest run of them)."""
+    n, run = _i(), _i()
+    _check(lib.pv_kv_free_pages(kv, ctypes.byref(n), ctypes.byref(run)))
+    return n.value, run.value
+
+
 def pv_rope_append(kv, streams, layer, step, q, k, v, q_rot, cuda_stream=None) -> None:
     n, arr = _streams(streams)
     _check(lib.pv_rope_append(kv, n, arr, layer, step, _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot),
@@ -201,6 +275,58 @@ def pv_chunk_attn(kv, streams, layer, step, q_rot, out, lse=None, cuda_stream=No
     n, arr = _streams(streams)
     _check(lib.pv_chunk_attn(kv, n, arr, layer, step, _ptr(q_rot), _ptr(out), _ptr(lse),
                              _stream(cuda_stream)))
+
+
+def pv_kv_summary_bytes(kv) -> int:
+    a = _sz()
+    _check(lib.pv_kv_summary_bytes(kv, ctypes.byref(a)))
+    return a.value
+
+
+def pv_kv_set_summaries(kv, summ, nbytes=0) -> None:
+    _check(lib.pv_kv_set_summaries(kv, _ptr(summ), nbytes))
+
+
+def pv_block_summarize(kv, streams, layer, step, cuda_stream=None) -> None:
+    n, arr = _streams(streams)
+    _check(lib.pv_block_summarize(kv, n, arr, layer, step, _stream(cuda_stream)))
+
+
+def pv_block_select(kv, streams, layer, step, q_rot, keep, force, blocks, cuda_stream=None) -> None:
+    n, arr = _streams(streams)
+    _check(lib.pv_block_select(kv, n, arr, layer, step, _dense(q_rot), keep, force, _dense(blocks),
+                               _stream(cuda_stream)))
+
+
+def pv_block_attn(kv, streams, layer, step, q_rot, blocks, keep, out, lse=None,
+                  cuda_stream=None) -> None:
+    n, arr = _streams(streams)
+    _check(lib.pv_block_attn(kv, n, arr, layer, step, _dense(q_rot), _dense(blocks), keep,
+                             _dense(out), _dense(lse), _stream(cuda_stream)))
+
+
+def pv_block_summarize_dense(k, n_k, heads, head_dim, means, cuda_stream=None) -> None:
+    _check(lib.pv_block_summarize_dense(_dense(k), n_k, heads, head_dim, _dense(means),
+                                        _stream(cuda_stream)))
+
+
+def pv_block_select_dense(q, means, n_q, n_k, heads, head_dim, keep, n_front, blocks,
+                          cuda_stream=None) -> None:
+    _check(lib.pv_block_select_dense(_dense(q), _dense(means), n_q, n_k, heads, head_dim, keep,
+                                     n_front, _dense(blocks), _stream(cuda_stream)))
+
+
+def pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep) -> int:
+    a = _sz()
+    _check(lib.pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep, ctypes.byref(a)))
+    return a.value
+
+
+def pv_block_attn_dense(q, k, v, n_q, n_k, heads, head_dim, blocks, keep, out, lse, ws, ws_bytes,
+                        cuda_stream=None) -> None:
+    _check(lib.pv_block_attn_dense(_dense(q), _dense(k), _dense(v), n_q, n_k, heads, head_dim,
+                                   _dense(blocks), keep, _dense(out), _dense(lse), _dense(ws),
+                                   ws_bytes, _stream(cuda_stream)))
 
 
 def pv_rope_dense(kv, n_tokens, frame0, q, k, v, q_rot, k_rot, v_hm, cuda_stream=None) -> None:
@@ -324,32 +450,54 @@ def pv_attn_selftest_wait_timeout(ws=None, cuda_stream=None) -> None:
 
 # ------------------------------------------------------------------ helpers
 class KVStore:
-    """Owns the caller-side device buffers (torch) of one pv_kv handle."""
+    """Owns the caller-side device buffers (torch) of one pv_kv handle.
 
-    def __init__(self, cfg: pv_kv_config, device="cuda"):
+    pages: pages of a paged store (None: fixed rows per stream).
+    summaries: attach block means (pv_block_summarize, pv_block_select)."""
+
+    def __init__(self, cfg: pv_kv_config, device="cuda", pages=None, summaries=False):
         import torch
         self.cfg = cfg
-        self.kv_bytes, self.ws_bytes = pv_kv_required_bytes(cfg)
+        self.pages = pages
+        if pages is None:
+            self.kv_bytes, self.ws_bytes = pv_kv_required_bytes(cfg)
+        else:
+            self.kv_bytes, self.ws_bytes = pv_kv_paged_required_bytes(cfg, pages)
         self.kv_buf = torch.empty(self.kv_bytes, dtype=torch.uint8, device=device)
         self.ws_buf = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-        self.handle = pv_kv_init(cfg, self.kv_buf, self.kv_bytes, self.ws_buf, self.ws_bytes)
+        bufs = (self.kv_buf, self.kv_bytes, self.ws_buf, self.ws_bytes)
+        self.handle = pv_kv_init(cfg, *bufs) if pages is None else pv_kv_init_paged(cfg, pages, *bufs)
         self.T = cfg.frame_w * cfg.frame_h
-        self.ltot = (cfg.first_frames + cfg.ring_slots) * self.T
+        self.ltot = (cfg.first_frames + cfg.ring_slots if pages is None else pages) * self.T
+        self.summ_buf = None
+        if summaries:
+            n = pv_kv_summary_bytes(self.handle)
+            self.summ_buf = torch.empty(n, dtype=torch.uint8, device=device)
+            pv_kv_set_summaries(self.handle, self.summ_buf, n)
+
+    def _shape(self, rows):
+        """[layers][steps][streams][heads][rows][D], without streams for a paged store."""
+        c = self.cfg
+        streams = (c.max_streams,) if self.pages is None else ()
+        return (c.layers, c.steps, *streams, c.heads, rows, c.head_dim)
 
     def k_region(self):
-        """The K region as bf16 [layers][steps][streams][heads][Ltot][D] (a view)."""
+        """The K region as bf16 [layers][steps][streams][heads][Ltot][D], for a paged store
+        [layers][steps][heads][pages * T][D] (a view)."""
         import torch
-        c = self.cfg
-        n = c.layers * c.steps * c.max_streams * c.heads * self.ltot * c.head_dim
         flat = self.kv_buf.view(torch.bfloat16)
-        return flat[:n].view(c.layers, c.steps, c.max_streams, c.heads, self.ltot, c.head_dim)
+        return flat[:flat.numel() // 2].view(self._shape(self.ltot))
 
     def v_region(self):
         import torch
-        c = self.cfg
-        n = c.layers * c.steps * c.max_streams * c.heads * self.ltot * c.head_dim
         flat = self.kv_buf.view(torch.bfloat16)
-        return flat[n:2 * n].view(c.layers, c.steps, c.max_streams, c.heads, self.ltot, c.head_dim)
+        return flat[flat.numel() // 2:].view(self._shape(self.ltot))
+
+    def summary_region(self):
+        """The block means as f32, like k_region with ceil(T / 128) rows per frame (a view)."""
+        import torch
+        rows = self.ltot // self.T * -(-self.T // PV_BLOCK_KEYS)
+        return self.summ_buf.view(torch.float32).view(self._shape(rows))
 
     def close(self):
         if self.handle:
