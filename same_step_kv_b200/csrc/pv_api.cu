@@ -1018,9 +1018,7 @@ pv_status check_same_device(const pv_kv_s* kv) {
 pv_status store_blocks(const pv_kv_s* kv, int n_streams, const int* streams, int layer, int step,
                        KeyBlocks* kb) {
     long long tok = 0;
-    kb->seg_len = kv->T;
-    kb->bps = blocks_per_seg(kv);
-    kb->tail = kv->T - (kb->bps - 1) * kKeyTile;
+    set_blocks(kb, kv->T);
     kb->head_segs = head_segs(kv);
     kb->first = kv->cfg.first_frames;
     for (int i = 0; i < n_streams; ++i) {
@@ -1478,9 +1476,7 @@ pv_status dense_blocks(int n_q, int n_k, int heads, int head_dim, int* nb) {
 }
 KeyBlocks one_segment(int n_k, int nb) {
     KeyBlocks kb{};
-    kb.seg_len = n_k;
-    kb.bps = nb;
-    kb.tail = n_k - (nb - 1) * kKeyTile;
+    set_blocks(&kb, n_k);
     kb.head_segs = 1;
     kb.n_blocks[0] = nb;
     return kb;

@@ -292,7 +292,27 @@ struct Seg {
     int which;     // 0: this CTA's first segment, 1: a later one
 };
 
+// Head and query block of a stream's item li.  Contiguous keys:
+// query-block-major, so that with a grid that is a multiple of n_qb the CTAs
+// working on one head's query blocks walk the same key tiles at the same time
+// and share them through L2.  Listed blocks: head-major; the query blocks of a
+// head read different blocks of the same keys, and the few heads that the
+// launch works on at a time fit in L2 with all their keys (24 heads, 18,480
+// tokens, 36 of 145 blocks: 931 us against 1,009 us query-block-major).
+template <bool kBlocks>
+__device__ __forceinline__ void item_place(const AttnParams& p, const AttnStreamDesc& s, int li,
+                                           Seg& g) {
+    if (kBlocks) {
+        g.head = li / s.n_qb;
+        g.qb = li - g.head * s.n_qb;
+    } else {
+        g.qb = li / p.heads;
+        g.head = li - g.qb * p.heads;
+    }
+}
+
 // The whole item `item` as one segment (items handed out at run time).
+template <bool kBlocks>
 __device__ __forceinline__ void item_seg(const AttnParams& p, int item, Seg& g) {
     int i = 0;
     while (i + 1 < p.n_streams && p.st[i + 1].item0 <= item) ++i;
@@ -301,8 +321,7 @@ __device__ __forceinline__ void item_seg(const AttnParams& p, int item, Seg& g) 
     g.si = i;
     g.kt0 = 0;
     g.n = s.n_kt;
-    g.qb = li / p.heads;
-    g.head = li - g.qb * p.heads;
+    item_place<kBlocks>(p, s, li, g);
     g.item = item;
     g.i0 = s.cost0 + (long long)li * s.n_kt;
     g.c_first = blockIdx.x;
@@ -313,6 +332,7 @@ __device__ __forceinline__ void item_seg(const AttnParams& p, int item, Seg& g) 
     g.rows[1] = max(0, min(kQRows, s.n_q - g.q0 - kQRows));
 }
 
+template <bool kBlocks>
 struct SegIter {
     long long pos, end;
     __device__ SegIter(const AttnParams& p) : pos(bound(p, blockIdx.x)), end(bound(p, blockIdx.x + 1)) {}
@@ -330,11 +350,7 @@ struct SegIter {
         const long long e = i1 < end ? i1 : end;
         g.n = (int)(e - pos);
         g.which = pos == bound(p, blockIdx.x) ? 0 : 1;
-        // items are laid out query-block-major: with a grid that is a multiple
-        // of n_qb, the CTAs working on one head's query blocks then walk the
-        // same key tiles at the same time and share them through L2
-        g.qb = li / p.heads;
-        g.head = li - g.qb * p.heads;
+        item_place<kBlocks>(p, s, li, g);
         g.item = s.item0 + li;
         g.i0 = i0;
         g.c_first = cta_of(p, i0);
@@ -351,6 +367,7 @@ struct SegIter {
 // index from counters[0] and passes it to the MMA warp and the eight softmax
 // warps through a ring of kRing shared-memory slots; -1 ends the list.
 // Slot k is written once the consumers have all released slot k - kRing.
+template <bool kBlocks>
 __device__ bool item_grab(const AttnParams& p, Bars* b, int& k, Seg& g, bool& ok) {
     const int s = k % kRing;
     if (k >= kRing && !(ok = mbar_wait(smem_u32(&b->ring_empty[s]), ((k / kRing) - 1) & 1, b, p.err)))
@@ -361,10 +378,11 @@ __device__ bool item_grab(const AttnParams& p, Bars* b, int& k, Seg& g, bool& ok
     mbar_arrive(smem_u32(&b->ring_full[s]));  // release: the slot's value is visible
     ++k;
     if (item < 0) return false;
-    item_seg(p, item, g);
+    item_seg<kBlocks>(p, item, g);
     return true;
 }
 // Warp-wide: the next slot of the ring.
+template <bool kBlocks>
 __device__ bool item_take(const AttnParams& p, Bars* b, int& k, Seg& g, bool& ok) {
     const int s = k % kRing;
     ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&b->ring_full[s]), (k / kRing) & 1, b, p.err));
@@ -374,7 +392,7 @@ __device__ bool item_take(const AttnParams& p, Bars* b, int& k, Seg& g, bool& ok
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&b->ring_empty[s]));
     ++k;
     if (item < 0) return false;
-    item_seg(p, item, g);
+    item_seg<kBlocks>(p, item, g);
     return true;
 }
 
@@ -412,7 +430,7 @@ using BlockRowOf = std::conditional_t<B::kBlocks, BlockRow<B>, NoRow>;
 // Keys of block b: 128, fewer in the last block of a segment, 0 if empty.
 __device__ __forceinline__ int block_keys(const KeyBlocks& k, int b) {
     if (b < 0) return 0;
-    return (b + 1) % k.bps == 0 ? k.tail : kKeyTile;
+    return ends_segment(k, b) ? k.tail : kKeyTile;
 }
 
 // ----------------------------------------------------------------- roles
@@ -426,9 +444,9 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUt
     int stage_ev[C::kStages]; // release event of the tile in each stage
     bool ok = true;
     int rk = 0;  // ring slots written
-    SegIter it(p);
+    SegIter<B::kBlocks> it(p);
     Seg g;
-    while (ok && (kRun ? item_grab(p, b, rk, g, ok) : it.next(p, g))) {
+    while (ok && (kRun ? item_grab<B::kBlocks>(p, b, rk, g, ok) : it.next(p, g))) {
         const AttnStreamDesc& s = p.st[g.si];
         const int ntile = g.rows[1] > 0 ? 2 : 1;
         // the previous segment's S products are done with the Q tiles
@@ -500,7 +518,7 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUt
     }
 }
 
-template <int D, bool kRun>
+template <int D, bool kRun, typename B>
 __device__ void mma_issuer(const AttnParams& p, uint8_t* smem, Bars* b, uint32_t tmem) {
     using C = Cfg<D>;
     // every lane waits; the vote reconverges the warp before the next issue
@@ -551,9 +569,9 @@ __device__ void mma_issuer(const AttnParams& p, uint8_t* smem, Bars* b, uint32_t
         return true;
     };
     int rk = 0;  // ring slots taken
-    SegIter it(p);
+    SegIter<B::kBlocks> it(p);
     Seg g;
-    while (ok && (kRun ? item_take(p, b, rk, g, ok) : it.next(p, g))) {
+    while (ok && (kRun ? item_take<B::kBlocks>(p, b, rk, g, ok) : it.next(p, g))) {
         const bool hasB = g.rows[1] > 0;
         if (!(ok = wwait(smem_u32(&b->q_full), qseg & 1, b, p.err))) break;
         ++qseg;
@@ -631,11 +649,11 @@ __device__ __forceinline__ float exp_half(const uint32_t* sr, float2 sl2x2, floa
     return a.x + a.y;
 }
 
-// The same for listed blocks, with P rounded to nearest (half an ulp of the
-// last kept bit added before the byte permute; the same instruction count as
-// the truncation above) and the sum taken over the unrounded f32 values: the
-// rounding errors of P then average out in O, and the log-sum-exp keeps f32
-// accuracy.
+// The same for listed blocks, with P rounded to nearest and the sum taken
+// over the unrounded f32 values: the rounding errors of P then average out in
+// O, and the log-sum-exp keeps f32 accuracy.  One packed conversion costs what
+// the byte permute of a truncation does (69.1 us either way for a chunk of
+// 880 queries over 37 blocks; adding half an ulp before a permute: 72.8 us).
 __device__ __forceinline__ float exp_half_rn(const uint32_t* sr, float2 sl2x2, float2 nmx2,
                                              uint32_t tP) {
     float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
@@ -646,7 +664,7 @@ __device__ __forceinline__ float exp_half_rn(const uint32_t* sr, float2 sl2x2, f
                                     sl2x2, nmx2);
         const float2 e = make_float2(ex2(x.x), ex2(x.y));
         acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], e);
-        pk[i / 2] = __byte_perm(__float_as_uint(e.x) + 0x8000u, __float_as_uint(e.y) + 0x8000u, 0x7632);
+        pk[i / 2] = pack_bf16(e.x, e.y);
     }
     tmem_st32(tP, pk);
     const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
@@ -850,9 +868,9 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
     int ec = 0;   // split epilogues, for the ep_in / ep_out phases
     bool ok = true;
     int rk = 0;  // ring slots taken
-    SegIter it(p);
+    SegIter<B::kBlocks> it(p);
     Seg g;
-    while (ok && (kRun ? item_take(p, b, rk, g, ok) : it.next(p, g))) {
+    while (ok && (kRun ? item_take<B::kBlocks>(p, b, rk, g, ok) : it.next(p, g))) {
         if (g.rows[X] == 0) continue;  // this segment has no query tile X
         const AttnStreamDesc& s = p.st[g.si];
         float m = -INFINITY;  // maximum applied to the exponentials, log2 units
@@ -1074,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             if (lane_id == 0) producer<D, kRun>(&tq, &tk, &tv, p, ba, smem, b);
         } else if (warp == 1) {
-            mma_issuer<D, kRun>(p, smem, b, tmem);  // the whole warp; one elected lane issues
+            mma_issuer<D, kRun, B>(p, smem, b, tmem);  // the whole warp; one elected lane issues
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));

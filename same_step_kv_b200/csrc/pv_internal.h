@@ -113,11 +113,25 @@ cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 // page table in a paged store.
 struct KeyBlocks {
     int seg_len, bps, tail;
+    unsigned long long bps_inv;    // ceil(2^64 / bps), for ends_segment
     int head_segs;       // physical segments between heads
     int first;           // segments of the sink run (paged store)
     int seg0[PV_MAX_STREAMS];      // physical segment of head 0, page 0
     int n_blocks[PV_MAX_STREAMS];
 };
+// Whether block b is the last of its segment: (b + 1) is a multiple of bps,
+// tested without a division (Lemire, Kaser, Kurz, "Faster remainder by direct
+// computation", 2019: d divides n iff n * ceil(2^64 / d) mod 2^64 is below
+// ceil(2^64 / d), for 32-bit n and d).
+__host__ __device__ inline bool ends_segment(const KeyBlocks& k, int b) {
+    return (unsigned long long)(unsigned)(b + 1) * k.bps_inv <= k.bps_inv - 1;
+}
+inline void set_blocks(KeyBlocks* k, int seg_len) {
+    k->seg_len = seg_len;
+    k->bps = (seg_len + kKeyTile - 1) / kKeyTile;
+    k->tail = seg_len - (k->bps - 1) * kKeyTile;
+    k->bps_inv = ~0ull / (unsigned)k->bps + 1;   // 0, that is 2^64, for one block
+}
 struct FixedRows {
     __host__ __device__ static int page(const KeyBlocks&, int, int seg) { return seg; }
 };
