@@ -1042,18 +1042,64 @@ void fill_pages(const pv_kv_s* kv, int n_streams, const int* streams, PageTable*
     }
 }
 
+// What a launch over listed blocks needs besides AttnParams.
+struct BlockCall {
+    const void *q, *k, *v;
+    CUtensorMap tq, tk, tv, to;
+    const int* list;
+    int keep;
+    int list_row0[PV_MAX_STREAMS];
+    KeyBlocks kb;
+    size_t part_floats;     // workspace: partial results and arrival counters
+    int n_partials, n_counters;
+    int n_sm;
+};
+// The kernel by query count: mma.sync with keys straight to registers for a
+// few queries, 128-row tcgen05 tiles for more.
 template <typename Pages>
-cudaError_t launch_store_blocks(pv_kv kv, const CUtensorMap& tq, const CUtensorMap& to,
-                                const AttnParams& p, const int* blocks, int keep,
-                                const int* list_row0, const KeyBlocks& kb, const Pages& pages,
-                                cudaStream_t s) {
+pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, cudaStream_t s) {
+    int most = 0;
+    for (int i = 0; i < p.n_streams; ++i) most = std::max(most, p.st[i].n_q);
+    if (most <= kFewQueries) {
+        FewArgs<Pages> f{};
+        for (int i = 0; i < p.n_streams; ++i) {
+            f.st[i].n_q = p.st[i].n_q;
+            f.st[i].q_row0 = p.st[i].q_row0;
+            f.st[i].out_tok0 = p.st[i].out_tok0;
+            f.st[i].n_sel = p.st[i].n_k / kKeyTile;
+        }
+        int ctas = 0;
+        if (plan_few(f.st, p.n_streams, p.heads, p.head_dim, c.n_sm, c.part_floats, c.n_counters,
+                     &f.per, &ctas)) {
+            f.q = (const bf16*)c.q;
+            f.k = (const bf16*)c.k;
+            f.v = (const bf16*)c.v;
+            f.out = p.out;
+            f.lse = p.lse;
+            f.partial = p.partial;
+            f.counters = p.counters;
+            f.heads = p.heads;
+            f.n_streams = p.n_streams;
+            f.scale_log2 = p.scale_log2;
+            f.list = c.list;
+            f.keep = c.keep;
+            std::copy(c.list_row0, c.list_row0 + p.n_streams, f.list_row0);
+            f.kb = c.kb;
+            f.pages = pages;
+            const cudaError_t e = launch_few(f, p.head_dim, ctas, s);
+            return e == cudaSuccess ? PV_OK : cuda_fail(e, "block attention launch");
+        }
+    }
+    if (plan_attention(p, c.n_sm, c.n_partials, c.n_counters) < 0)
+        return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
     BlockArgs<Pages> b{};
-    b.list = blocks;
-    b.keep = keep;
-    std::copy(list_row0, list_row0 + p.n_streams, b.list_row0);
-    b.kb = kb;
+    b.list = c.list;
+    b.keep = c.keep;
+    std::copy(c.list_row0, c.list_row0 + p.n_streams, b.list_row0);
+    b.kb = c.kb;
     b.pages = pages;
-    return launch_block_attn(tq, kv->tm_k3, kv->tm_v3, to, p, b, s);
+    const cudaError_t e = launch_block_attn(c.tq, c.tk, c.tv, c.to, p, b, s);
+    return e == cudaSuccess ? PV_OK : cuda_fail(e, "block attention launch");
 }
 
 // Attention of the listed streams at (layer, step): over the listed blocks,
@@ -1078,9 +1124,8 @@ pv_status store_attn(pv_kv kv, int n_streams, const int* streams, int layer, int
     std::lock_guard<std::mutex> lock(kv->mu);
     for (int i = 0; i < n_streams; ++i)
         if ((st = check_read_phase(kv->streams[streams[i]], streams[i], step))) return st;
-    KeyBlocks kb{};
-    if (by_block && (st = store_blocks(kv, n_streams, streams, layer, step, &kb))) return st;
-    int list_row0[PV_MAX_STREAMS];
+    BlockCall call{};
+    if (by_block && (st = store_blocks(kv, n_streams, streams, layer, step, &call.kb))) return st;
     long long list_rows = 0;
     AttnParams p{};
     p.out = (bf16*)out;
@@ -1101,31 +1146,42 @@ pv_status store_attn(pv_kv kv, int n_streams, const int* streams, int layer, int
         a.n_q = d.n_queries;
         // block by block, the plan counts the stream's tiles as full ones
         a.n_k = !by_block ? d.n_keys
-                          : kKeyTile * (blocks ? std::min(keep, kb.n_blocks[i]) : kb.n_blocks[i]);
+                          : kKeyTile * (blocks ? std::min(keep, call.kb.n_blocks[i])
+                                               : call.kb.n_blocks[i]);
         a.q_row0 = c.heads * tok;
         a.kv_row0 = (int)base_row(kv, layer, step == PV_STEP_SINK ? 0 : step, streams[i]);
         a.kv_head_stride = kv->ltot;
         a.out_tok0 = tok;
-        list_row0[i] = (int)list_rows;
+        call.list_row0[i] = (int)list_rows;
         list_rows += (long long)c.heads * ((d.n_queries + kQBlock - 1) / kQBlock);
         tok += d.n_queries;
     }
-    if (plan_attention(p, kv->n_sm, kv->wl.n_partials, kv->wl.n_counters) < 0)
-        return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
     CUtensorMap tq, to;
     if ((st = q_map(kv, q_rot, (long long)c.heads * tok, &tq))) return st;
     if ((st = out_map(kv, out, tok, &to))) return st;
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    cudaError_t e;
-    if (!by_block) {
-        e = launch_attn(tq, kv->tm_k, kv->tm_v, to, p, s);
-    } else if (kv->n_pages > 0) {
+    if (by_block) {
+        call.q = q_rot;
+        call.k = kv->kbase;
+        call.v = kv->vbase;
+        call.tq = tq;
+        call.tk = kv->tm_k3;
+        call.tv = kv->tm_v3;
+        call.to = to;
+        call.list = blocks;
+        call.keep = keep;
+        call.part_floats = (kv->wl.total - kv->wl.part_off) / sizeof(float);
+        call.n_partials = kv->wl.n_partials;
+        call.n_counters = kv->wl.n_counters;
+        call.n_sm = kv->n_sm;
+        if (kv->n_pages == 0) return launch_blocks(p, call, FixedRows{}, s);
         PageTable pages;
         fill_pages(kv, n_streams, streams, &pages);
-        e = launch_store_blocks(kv, tq, to, p, blocks, keep, list_row0, kb, pages, s);
-    } else {
-        e = launch_store_blocks(kv, tq, to, p, blocks, keep, list_row0, kb, FixedRows{}, s);
+        return launch_blocks(p, call, pages, s);
     }
+    if (plan_attention(p, kv->n_sm, kv->wl.n_partials, kv->wl.n_counters) < 0)
+        return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
+    const cudaError_t e = launch_attn(tq, kv->tm_k, kv->tm_v, to, p, s);
     if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
     return PV_OK;
 }
@@ -1386,7 +1442,6 @@ pv_status pv_block_summarize(pv_kv kv, int n_streams, const int* streams, int la
         items += (long long)p.n_segs[i] * p.bps;
         if (items >= (1LL << 31)) return fail(PV_ERR_SHAPE, "too many blocks in one call");
     }
-    if (c.heads > 65535) return fail(PV_ERR_SHAPE, "more than 65535 heads");
     p.n_items = (int)items;
     const cudaError_t e = launch_summary(p, (cudaStream_t)cuda_stream);
     if (e != cudaSuccess) return cuda_fail(e, "block means launch");
@@ -1490,7 +1545,6 @@ pv_status pv_block_summarize_dense(const void* k, int n_k, int heads, int head_d
     int nb = 0;
     pv_status st = dense_blocks(1, n_k, heads, head_dim, &nb);
     if (st) return st;
-    if (heads > 65535) return fail(PV_ERR_SHAPE, "more than 65535 heads");
     if (!k || !means) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
     if (!aligned(k, 16) || !aligned(means, 16))
         return fail(PV_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
@@ -1596,22 +1650,24 @@ pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n
     p.n_streams = 1;
     p.st[0].n_q = n_q;
     p.st[0].n_k = n_sel * kKeyTile;
-    if (plan_attention(p, n_sm, n_part, n_cnt) < 0)
-        return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
-    BlockArgs<FixedRows> b{};
-    b.list = blocks;
-    b.keep = keep;
-    b.kb = one_segment(n_k, nb);
-    CUtensorMap tq, tk, tv, to;
+    BlockCall call{};
+    call.q = q;
+    call.k = k;
+    call.v = v;
+    call.list = blocks;
+    call.keep = keep;
+    call.kb = one_segment(n_k, nb);
+    call.part_floats = n_part * partial_slot_floats(head_dim);
+    call.n_partials = n_part;
+    call.n_counters = n_cnt;
+    call.n_sm = n_sm;
     char msg[256];
-    if (!encode_rows_map(&tq, q, (long long)heads * n_q, head_dim, msg, sizeof msg) ||
-        !encode_seg_map(&tk, k, n_k, heads, head_dim, msg, sizeof msg) ||
-        !encode_seg_map(&tv, v, n_k, heads, head_dim, msg, sizeof msg) ||
-        !encode_out_map(&to, out, n_q, heads, head_dim, msg, sizeof msg))
+    if (!encode_rows_map(&call.tq, q, (long long)heads * n_q, head_dim, msg, sizeof msg) ||
+        !encode_seg_map(&call.tk, k, n_k, heads, head_dim, msg, sizeof msg) ||
+        !encode_seg_map(&call.tv, v, n_k, heads, head_dim, msg, sizeof msg) ||
+        !encode_out_map(&call.to, out, n_q, heads, head_dim, msg, sizeof msg))
         return fail(PV_ERR_CUDA, "%s", msg);
-    const cudaError_t e = launch_block_attn(tq, tk, tv, to, p, b, (cudaStream_t)cuda_stream);
-    if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
-    return PV_OK;
+    return launch_blocks(p, call, FixedRows{}, (cudaStream_t)cuda_stream);
 }
 
 pv_status pv_rope_dense(pv_kv kv, int n_tokens, int frame0, const void* q, const void* k,

@@ -12,6 +12,15 @@
 #include <cooperative_groups.h>
 
 #include "pv_internal.h"
+#ifndef PV_LB
+#define PV_LB 3
+#endif
+#ifndef PV_SLB
+#define PV_SLB 3
+#endif
+#ifndef PV_QS
+#define PV_QS 0
+#endif
 
 namespace cg = cooperative_groups;
 
@@ -21,68 +30,126 @@ namespace {
 constexpr int kPoolThreads = 256;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
-// Adds eight bf16 values (one 16-byte load) to f64 sums.
-__device__ __forceinline__ void add8(double* a, const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Adds rows x and y (eight bf16 columns each) to f64 sums.  The conversions
+// to f64 share a slow pipe, so two values are added in f32 first and converted
+// once, wherever that addition is exact: s = x + y is, when both s - x == y
+// and s - y == x (of the two, the difference with the larger operand is
+// exact in f32, and equal to the other operand only if nothing was lost).
+// For values within about 16 binades of one another it always is.
+__device__ __forceinline__ void add_rows(double* a, const uint4& x4, const uint4& y4) {
+    const uint32_t xs[4] = {x4.x, x4.y, x4.z, x4.w}, ys[4] = {y4.x, y4.y, y4.z, y4.w};
+    const float2 neg = make_float2(-1.f, -1.f);
+    float2 s[4];
+    uint32_t lost = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        a[2 * i] += (double)__uint_as_float(w[i] << 16);
-        a[2 * i + 1] += (double)__uint_as_float(w[i] & 0xFFFF0000u);
+        const float2 x = bf16_pair(xs[i]), y = bf16_pair(ys[i]);
+        s[i] = __fadd2_rn(x, y);
+        const float2 d = __ffma2_rn(y, neg, __ffma2_rn(x, neg, s[i]));
+        const float2 e = __ffma2_rn(x, neg, __ffma2_rn(y, neg, s[i]));
+        lost |= __float_as_uint(d.x) | __float_as_uint(e.x);
+        lost |= __float_as_uint(d.y) | __float_as_uint(e.y);
+    }
+    if (lost == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[2 * i] += (double)s[i].x;
+            a[2 * i + 1] += (double)s[i].y;
+        }
+    } else {  // also sums beyond f32, infinities and NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = bf16_pair(xs[i]), y = bf16_pair(ys[i]);
+            a[2 * i] = a[2 * i] + (double)x.x + (double)y.x;
+            a[2 * i + 1] = a[2 * i + 1] + (double)x.y + (double)y.y;
+        }
     }
 }
 
-// Sums of the rows [r0, r1) of `rows` (bf16 [.][D]), D columns, by the whole
-// block, at most kRows of them: partial sums of the warps in part [kPoolWarps][D];
-// the caller synchronises.
+// Sums of rows [r0, r1), at most kRows of them, over a strip of 64 columns by
+// one warp: `strip` points at the strip's first column of row 0, rows are D
+// apart.  Lanes 0..7 end with columns 8 lane .. 8 lane + 7.
 template <int D, int kRows>
-__device__ __forceinline__ void pool_rows(const bf16* rows, int r0, int r1, double* part) {
-    constexpr int kLanes = D / 8;                    // threads across one row
-    constexpr int kStep = kPoolThreads / kLanes;     // rows per pass
-    constexpr int kPasses = (kRows + kStep - 1) / kStep;
-    const int col = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-    uint4 v[kPasses];
+__device__ __forceinline__ void pool_strip(const bf16* strip, int r0, int r1, double* a) {
+    constexpr int kLoads = kRows >= 32 ? 8 : (kRows + 3) / 4;   // in flight, four rows each
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int r = r0 + row + i * kStep;
-        v[i] = r < r1 ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * D) + col)
-                      : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < 8; ++c) a[c] = 0.0;
+#pragma unroll 1
+    for (int r = r0 + lane / 8; r < r0 + kRows; r += 4 * kLoads) {
+        uint4 v[kLoads + kLoads % 2];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            v[i] = r + 4 * i < r1
+                       ? __ldg(reinterpret_cast<const uint4*>(strip + (size_t)(r + 4 * i) * D) + (lane & 7))
+                       : make_uint4(0, 0, 0, 0);
+        if (kLoads % 2) v[kLoads] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kLoads; i += 2) add_rows(a, v[i], v[i + 1]);
     }
-    double a[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) add8(a, v[i]);
+    for (int m = 8; m < 32; m *= 2)
 #pragma unroll
-    for (int m = kLanes; m < 32; m *= 2)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], m);
-    if ((threadIdx.x & 31) < kLanes) {
-        double* p = part + (threadIdx.x / 32) * D + col * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = a[i];
-    }
+        for (int c = 0; c < 8; ++c) a[c] += __shfl_xor_sync(0xffffffffu, a[c], m);
 }
 
-// One CTA per (block of a run, head, plane).  Bound by reading the keys.
-template <int D>
-__global__ void __launch_bounds__(kPoolThreads)
+// kParts warps share the rows of each (block, strip).  Four: the fewest steps
+// one after the other, for few blocks.  One: long streams of loads without a
+// synchronisation, for many.  Bound by reading the keys.
+template <int D, int kParts>
+__global__ void __launch_bounds__(kPoolThreads, PV_SLB)
     summary_kernel(const __grid_constant__ SummaryParams p) {
-    __shared__ double part[kPoolWarps * D];
-    const int head = blockIdx.y;
-    const int item = blockIdx.x;
-    int i = 0;
-    while (i + 1 < p.n_runs && p.item0[i + 1] <= item) ++i;
-    const int li = item - p.item0[i];
-    const int seg = li / p.bps, blk = li - seg * p.bps;
-    const long long ps =
-        (long long)blockIdx.z * p.plane_segs + p.seg0[i] + (long long)head * p.head_segs + seg;
-    const int r0 = blk * kKeyTile;
-    const int r1 = min(p.seg_len, r0 + kKeyTile);
-    pool_rows<D, kKeyTile>(p.k + ps * p.seg_len * D, r0, r1, part);
-    __syncthreads();
-    if (threadIdx.x < D) {
-        double s = 0;
+    constexpr int kStrips = D / 64;
+    constexpr int kPer = kPoolWarps / (kStrips * kParts);    // blocks of a CTA
+    __shared__ double part[kParts > 1 ? kPoolWarps * 64 : 1];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int strip = warp / kParts % kStrips, share = warp % kParts;
+    const long long idx = (long long)blockIdx.x * kPer + warp / (kStrips * kParts);
+    const bool live = idx < (long long)p.n_items * p.heads;
+    float* dst = nullptr;
+    int rows = 0;
+    double a[8];
+    if (live) {
+        const int head = (int)(idx / p.n_items), item = (int)(idx - (long long)head * p.n_items);
+        int i = 0;
+        while (i + 1 < p.n_runs && p.item0[i + 1] <= item) ++i;
+        const int li = item - p.item0[i];
+        const int seg = li / p.bps, blk = li - seg * p.bps;
+        const long long ps =
+            (long long)blockIdx.y * p.plane_segs + p.seg0[i] + (long long)head * p.head_segs + seg;
+        rows = min(p.seg_len - blk * kKeyTile, kKeyTile);
+        dst = p.means + (ps * p.bps + blk) * D + strip * 64;
+        const bf16* src = p.k + (ps * p.seg_len + blk * kKeyTile) * D + strip * 64;
+        pool_strip<D, kKeyTile / kParts>(src, share * (kKeyTile / kParts),
+                                         min(rows, (share + 1) * (kKeyTile / kParts)), a);
+    }
+    if constexpr (kParts == 1) {
+        if (live && lane < 8) {
+            float m[8];
 #pragma unroll
-        for (int w = 0; w < kPoolWarps; ++w) s += part[w * D + threadIdx.x];
-        p.means[(ps * p.bps + blk) * D + threadIdx.x] = (float)(s / (double)(r1 - r0));
+            for (int c = 0; c < 8; ++c) m[c] = (float)(a[c] / (double)rows);
+            float4* d4 = reinterpret_cast<float4*>(dst) + lane * 2;
+            d4[0] = make_float4(m[0], m[1], m[2], m[3]);
+            d4[1] = make_float4(m[4], m[5], m[6], m[7]);
+        }
+    } else {
+        if (live && lane < 8) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) part[warp * 64 + lane * 8 + c] = a[c];
+        }
+        __syncthreads();
+        // the first warps of each (block, strip) add up its shares
+        if (live && share < 2) {
+            const int c = share * 32 + lane;
+            double s = 0;
+#pragma unroll
+            for (int w = 0; w < kParts; ++w) s += part[(warp - share + w) * 64 + c];
+            dst[c] = (float)(s / (double)rows);
+        }
     }
 }
 
@@ -180,14 +247,27 @@ __device__ void write_top(const unsigned long long* keys, int n, int n_sel, int 
                           int* out) {
     const int t = threadIdx.x;
     if (n <= kRankBlocks) {
-        // every thread counts the keys ahead of its own
+        // every thread counts the keys ahead of its own: equal ones before it,
+        // larger ones anywhere (keys holds a 0 behind an odd n)
         bool f = false;
         if (t < n) {
             const unsigned long long k = keys[t];
+            const int w0 = t & ~31, w1 = min(n, w0 + 32);
+            const ulonglong2* two = reinterpret_cast<const ulonglong2*>(keys);
             int ahead = 0;
-            for (int i = 0; i < n; ++i) {
+#pragma unroll 4
+            for (int i = 0; i < w0 / 2; ++i) {
+                const ulonglong2 o = two[i];
+                ahead += (o.x >= k) + (o.y >= k);
+            }
+            for (int i = w0; i < w1; ++i) {
                 const unsigned long long o = keys[i];
                 ahead += o > k || (o == k && i < t);
+            }
+#pragma unroll 4
+            for (int i = (w1 + 1) / 2; i < (n + 1) / 2; ++i) {
+                const ulonglong2 o = two[i];
+                ahead += (o.x > k) + (o.y > k);
             }
             f = ahead < n_sel;
         }
@@ -218,20 +298,24 @@ __device__ void write_top(const unsigned long long* keys, int n, int n_sel, int 
     for (int i = n_sel + t; i < keep; i += kSelThreads) out[i] = -1;
 }
 
-// One cluster of CTAs per (stream, head, query group): its CTAs share the
-// group's rows (sums exchanged through distributed shared memory) and the
+// A cluster of kCluster CTAs per (stream, head, query group).  Its CTAs share
+// the group's rows (sums exchanged through distributed shared memory) and the
 // blocks to score; the first one picks the top.
-template <int D, typename Pages>
-__global__ void __launch_bounds__(kSelThreads)
+template <int D, int kCluster, typename Pages>
+__global__ void __launch_bounds__(kSelThreads, PV_LB)
     select_kernel(const __grid_constant__ SelectParams p, const __grid_constant__ Pages pages) {
     cg::cluster_group cl = cg::this_cluster();
-    const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    extern __shared__ unsigned long long keys[];      // max_blocks
-    __shared__ double part[kPoolWarps * D];
+    const int rank = kCluster > 1 ? (int)cl.block_rank() : 0;
+    extern __shared__ __align__(16) unsigned long long keys[];   // max_blocks, rounded up to even
+    constexpr int kStrips = D / 64;
+    constexpr int kParts = kSelWarps / kStrips;       // warps that share a strip's rows
+    constexpr int kShare = kQBlock / kCluster;        // rows of a CTA
+    __shared__ double part[kParts * D];
     __shared__ double mine[D];                        // this CTA's sums
     __shared__ double qm[D];
     __shared__ SelShared sh;
-    const int item = blockIdx.x / cs;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int item = blockIdx.x / kCluster;
     int i = 0;
     while (i + 1 < p.n_streams && p.item0[i + 1] <= item) ++i;
     const int li = item - p.item0[i];
@@ -241,88 +325,84 @@ __global__ void __launch_bounds__(kSelThreads)
 
     // the group's mean query
     const int q0 = g * kQBlock, q1 = min(n_q, q0 + kQBlock);
-    const int share = kQBlock / cs;
-    const bf16* q = p.q + (p.q_row0[i] + (long long)head * n_q) * D;
     {
-        const int r0 = q0 + rank * share, r1 = min(q1, r0 + share);
-        if (cs >= 8)
-            pool_rows<D, kQBlock / 8>(q, r0, r1, part);
-        else
-            for (int r = r0; r < r0 + share; r += kQBlock / 4) {
-                // rows in runs of 64, the warps' sums added up
-                if (r > r0) __syncthreads();
-                pool_rows<D, kQBlock / 4>(q, r, min(r1, r + kQBlock / 4), part);
-                __syncthreads();
-                if (threadIdx.x < D) {
-                    double s = r > r0 ? mine[threadIdx.x] : 0.0;
+        const int strip = warp / kParts, share = warp % kParts;
+        const bf16* q = p.q + (p.q_row0[i] + (long long)head * n_q) * D + strip * 64;
+        const int r0 = q0 + rank * kShare + share * (kShare / kParts);
+        double a[8];
+        pool_strip<D, kShare / kParts>(q, r0, min(q1, r0 + kShare / kParts), a);
+        if (lane < 8) {
 #pragma unroll
-                    for (int w = 0; w < kPoolWarps; ++w) s += part[w * D + threadIdx.x];
-                    mine[threadIdx.x] = s;
-                }
-            }
-        if (cs >= 8) {
-            __syncthreads();
-            if (threadIdx.x < D) {
-                double s = 0;
-#pragma unroll
-                for (int w = 0; w < kPoolWarps; ++w) s += part[w * D + threadIdx.x];
-                mine[threadIdx.x] = s;
-            }
+            for (int c = 0; c < 8; ++c) part[share * D + strip * 64 + lane * 8 + c] = a[c];
         }
-    }
-    cl.sync();
-    if (threadIdx.x < D) {
-        double s = 0;
-        for (int r = 0; r < cs; ++r) s += cl.map_shared_rank(mine, r)[threadIdx.x];
-        qm[threadIdx.x] = (double)(float)(s / (double)(q1 - q0));
     }
     __syncthreads();
-
-    // scores of this CTA's blocks, to the first CTA
-    constexpr int kPer = D / 32;   // columns of a lane
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    double ql[kPer];
+    double sum = 0;
+    if (threadIdx.x < D) {
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) ql[c] = qm[lane * kPer + c];
-    unsigned long long* dst = cl.map_shared_rank(keys, 0);
-    const int n = p.kb.n_blocks[i];
-    const long long hs = p.kb.seg0[i] + (long long)head * p.kb.head_segs;
-    const int step = cs * kSelWarps;
-    for (int b0 = rank * kSelWarps + warp; b0 < n; b0 += 4 * step) {
-        float m[4][kPer];
+        for (int w = 0; w < kParts; ++w) sum += part[w * D + threadIdx.x];
+    }
+    if (kCluster > 1) {
+        if (threadIdx.x < D) mine[threadIdx.x] = sum;
+        cl.sync();
+        if (threadIdx.x < D) {
+            sum = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int b = b0 + u * step;
-            if (b < n) {
-                const int seg = b / p.kb.bps;
-                const long long row =
-                    (hs + pages.page(p.kb, i, seg)) * p.kb.bps + (b - seg * p.kb.bps);
-                const float* src = p.means + row * D + lane * kPer;
-                if constexpr (kPer == 4) {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-                    m[u][0] = v.x, m[u][1] = v.y, m[u][2] = v.z, m[u][3] = v.w;
-                } else {
-                    const float2 v = __ldg(reinterpret_cast<const float2*>(src));
-                    m[u][0] = v.x, m[u][1] = v.y;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int b = b0 + u * step;
-            if (b < n) {   // the same for the whole warp
-                double s = 0;
-#pragma unroll
-                for (int c = 0; c < kPer; ++c) s = fma(ql[c], (double)m[u][c], s);
-#pragma unroll
-                for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-                const bool forced = (b >= p.force0[i][0] && b < p.force1[i][0]) ||
-                                    (b >= p.force0[i][1] && b < p.force1[i][1]);
-                if (lane == 0) dst[b] = forced ? ~0ull : order_key(s);
-            }
+            for (int r = 0; r < kCluster; ++r) sum += cl.map_shared_rank(mine, r)[threadIdx.x];
         }
     }
-    cl.sync();
+    if (threadIdx.x < D) qm[threadIdx.x] = (double)(float)(sum / (double)(q1 - q0));
+    __syncthreads();
+
+    // scores of this CTA's blocks, to the first CTA: eight lanes to a block,
+    // each with every eighth run of four columns
+    constexpr int kRuns = D / 32;
+    const int l8 = lane & 7;
+    double ql[kRuns][4];
+#pragma unroll
+    for (int c = 0; c < kRuns; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ql[c][k] = qm[(c * 8 + l8) * 4 + k];
+    unsigned long long* dst = kCluster > 1 ? cl.map_shared_rank(keys, 0) : keys;
+    const int n = p.kb.n_blocks[i];
+    const long long hs = p.kb.seg0[i] + (long long)head * p.kb.head_segs;
+    for (int b0 = (rank * kSelWarps + warp) * 4; b0 < n; b0 += kCluster * kSelWarps * 4) {
+        const int b = b0 + lane / 8;
+        double s = 0, s2 = 0;
+        if (b < n) {
+            const int seg = b / p.kb.bps;
+            const long long row = (hs + pages.page(p.kb, i, seg)) * p.kb.bps + (b - seg * p.kb.bps);
+            const float4* src = reinterpret_cast<const float4*>(p.means + row * D) + l8;
+            float4 m[kRuns];
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c) m[c] = __ldg(src + c * 8);
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c) {
+                double2 qa = make_double2(ql[c][0], ql[c][1]), qb = make_double2(ql[c][2], ql[c][3]);
+                if (PV_QS) {
+                    const volatile double2* q2 = reinterpret_cast<const volatile double2*>(qm + (c * 8 + l8) * 4);
+                    qa.x = q2[0].x; qa.y = q2[0].y; qb.x = q2[1].x; qb.y = q2[1].y;
+                }
+                s = fma(qa.x, (double)m[c].x, s);
+                s2 = fma(qa.y, (double)m[c].y, s2);
+                s = fma(qb.x, (double)m[c].z, s);
+                s2 = fma(qb.y, (double)m[c].w, s2);
+            }
+            s += s2;
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (l8 == 0 && b < n) {
+            const bool forced = (b >= p.force0[i][0] && b < p.force1[i][0]) ||
+                                (b >= p.force0[i][1] && b < p.force1[i][1]);
+            dst[b] = forced ? ~0ull : order_key(s);
+        }
+    }
+    if (rank == 0 && threadIdx.x == 0 && (n & 1)) keys[n] = 0;
+    if (kCluster > 1)
+        cl.sync();
+    else
+        __syncthreads();
     if (rank == 0)
         write_top(keys, n, min(p.keep, n), p.keep, &sh, p.blocks + (long long)item * p.keep);
 }
@@ -373,36 +453,61 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
 }
 
-template <int D, typename Pages>
-cudaError_t launch_select_d(const SelectParams& p, const Pages& pages, cudaStream_t s) {
+template <int D, int kCluster, typename Pages>
+cudaError_t launch_select_c(const SelectParams& p, const Pages& pages, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
-    cudaError_t e = smem_limit_once(select_kernel<D, Pages>, kMaxSelectBlocks * 8, configured);
+    cudaError_t e =
+        smem_limit_once(select_kernel<D, kCluster, Pages>, kMaxSelectBlocks * 8, configured);
     if (e != cudaSuccess) return e;
-    // few items: several CTAs to each, for latency; many: one each
-    const int cs = p.n_items <= 148 ? 8 : p.n_items <= 2 * 148 ? 4 : 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.n_items * cs);
+    cfg.gridDim = dim3((unsigned)p.n_items * kCluster);
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)p.max_blocks * 8;
+    cfg.dynamicSmemBytes = (size_t)(p.max_blocks + 1) / 2 * 16;
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cs;
+    at.val.clusterDim.x = kCluster;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D, Pages>, p, pages);
+    return cudaLaunchKernelEx(&cfg, select_kernel<D, kCluster, Pages>, p, pages);
+}
+
+#ifndef PV_CS
+#define PV_CS 0
+#endif
+template <int D, typename Pages>
+cudaError_t launch_select_d(const SelectParams& p, const Pages& pages, cudaStream_t s) {
+    int cs = p.n_items <= 148 ? 8 : p.n_items <= 2 * 148 ? 4 : 1;
+    if (PV_CS) cs = PV_CS;
+    if (cs == 8) return launch_select_c<D, 8>(p, pages, s);
+    if (cs == 4) return launch_select_c<D, 4>(p, pages, s);
+    if (cs == 2) return launch_select_c<D, 2>(p, pages, s);
+    return launch_select_c<D, 1>(p, pages, s);
+}
+
+#ifndef PV_SUM
+#define PV_SUM 0
+#endif
+template <int D, int kParts>
+cudaError_t launch_summary_p(const SummaryParams& p, cudaStream_t s) {
+    constexpr int kPer = kPoolWarps / (D / 64 * kParts);
+    const long long ctas = ((long long)p.n_items * p.heads + kPer - 1) / kPer;
+    if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+    summary_kernel<D, kParts><<<dim3((unsigned)ctas, p.planes), kPoolThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_summary_d(const SummaryParams& p, cudaStream_t s) {
+    bool few = (long long)p.n_items * p.heads * p.planes <= 4 * 148;
+    if (PV_SUM) few = PV_SUM == 4;
+    return few ? launch_summary_p<D, 4>(p, s) : launch_summary_p<D, 1>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_summary(const SummaryParams& p, cudaStream_t s) {
-    const dim3 grid(p.n_items, p.heads, p.planes);
-    if (p.head_dim == 128)
-        summary_kernel<128><<<grid, kPoolThreads, 0, s>>>(p);
-    else
-        summary_kernel<64><<<grid, kPoolThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.head_dim == 128 ? launch_summary_d<128>(p, s) : launch_summary_d<64>(p, s);
 }
 
 cudaError_t launch_select(const SelectParams& p, const PageTable* pages, cudaStream_t s) {

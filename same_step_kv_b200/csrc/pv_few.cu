@@ -1,0 +1,361 @@
+// Attention of few queries over listed key blocks: single tokens and other
+// short query sets, where the 128-row tiles of the tcgen05 kernel would be
+// almost empty and reading K and V is all the time there is.
+//
+// An item is (stream, head, 16 queries).  Its keys are cut into parts of
+// `per` units of 64 keys, one CTA of four warps to a part, so that few items
+// fill the GPU; a warp takes 16 keys of each unit.  Keys and values go from
+// global memory straight into the operand registers of mma.sync.m16n8k16
+// (M = the 16 queries): nothing is staged, so nothing waits at a barrier
+// inside the key loop, and a warp has its next keys in flight while it
+// works.  Running maximum and sum per warp as in the other kernels; the four
+// warps join through shared memory, the parts of an item through global
+// memory by the last CTA to arrive, in part order.
+//
+// Operand registers.  With g = lane / 4 and c = lane % 4, mma wants from a
+// lane A rows g, g + 8 and B column g, each at k = 2c, 2c + 1, 2c + 8, 2c + 9.
+//  S = Q K^T: the order of the k positions is free as long as Q and K agree,
+//   so lane c takes the 16-byte pieces c, c + 4, c + 8, ... of a row, eight
+//   dimensions that serve two k steps.
+//  O = P V: the order of the columns is free, so column g of tile t stands
+//   for column 8 g + t of a 64-column half, and a lane's eight tiles come
+//   from one 16-byte piece of each of its four key rows.
+#include "pv_internal.h"
+
+namespace pv {
+namespace {
+
+constexpr int kFewThreads = 128;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr float kFewEmpty = -3.0e38f;   // running maximum of a row without keys
+
+__device__ __forceinline__ float few_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t few_pack(float lo, float hi) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&b);
+}
+__device__ __forceinline__ uint4 few_load(const bf16* p, bool in) {
+    return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+
+template <int D>
+struct FewShared {
+    float o[kFewWarps][kFewRows][D];
+    float m[kFewWarps][kFewRows], l[kFewWarps][kFewRows];
+    int last;
+};
+
+// One row of an item from its parts' (m, l, o): acc = sum_i 2^(m_i - M) o_i,
+// L = sum_i 2^(m_i - M) l_i.
+struct FewRow {
+    float M, L;
+};
+
+template <int D, typename Pages>
+__global__ void __launch_bounds__(kFewThreads)
+    few_kernel(const __grid_constant__ FewArgs<Pages> p) {
+    __shared__ FewShared<D> sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int g = lane / 4, c = lane % 4;
+    constexpr int kPieces = D / 32;   // 16-byte pieces of a row per lane
+    constexpr int kHalves = D / 64;
+
+    int si = 0;
+    while (si + 1 < p.n_streams && p.st[si + 1].cta0 <= (int)blockIdx.x) ++si;
+    const FewStream& st = p.st[si];
+    const int li = blockIdx.x - st.cta0;
+    const int item = li / st.splits, split = li - item * st.splits;
+    const int tiles = (st.n_q + kFewRows - 1) / kFewRows;
+    const int head = item / tiles, rt = item - head * tiles;
+    const int row0 = rt * kFewRows, rows = min(kFewRows, st.n_q - row0);
+    const int groups = (st.n_q + kQBlock - 1) / kQBlock;
+    const int* list = p.list ? p.list + (p.list_row0[si] + (long long)head * groups +
+                                         row0 / kQBlock) * p.keep
+                             : nullptr;
+
+    // Q: rows g and g + 8
+    uint4 qa[kPieces], qb[kPieces];
+    {
+        const bf16* q = p.q + ((long long)st.q_row0 + (long long)head * st.n_q + row0) * D + c * 8;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            qa[i] = few_load(q + g * D + i * 32, g < rows);
+            qb[i] = few_load(q + (g + 8) * D + i * 32, g + 8 < rows);
+        }
+    }
+
+    // unit u: keys [64 (u % 2), + 64) of listed block u / 2; this warp's 16
+    // keys from row 16 warp on.  Rows of the block's first key, valid keys.
+    const long long base = (long long)p.kb.seg0[si] + (long long)head * p.kb.head_segs;
+    auto locate = [&](int u, long long* row, int* valid) {
+        const int b = list ? __ldg(list + u / 2) : u / 2;
+        const int k0 = (u % 2) * kFewUnit + warp * 16;
+        *row = 0;
+        *valid = 0;
+        if ((unsigned)b >= (unsigned)p.kb.n_blocks[si]) return;  // an empty block
+        const int seg = b / p.kb.bps, blk = b - seg * p.kb.bps;
+        *valid = (blk == p.kb.bps - 1 ? p.kb.tail : kKeyTile) - k0;
+        *row = (base + p.pages.page(p.kb, si, seg)) * p.kb.seg_len + blk * kKeyTile + k0;
+    };
+    uint4 kk[2][kPieces];       // keys g and g + 8 of the strip
+    uint4 vv[4][kHalves];       // values of keys 2c, 2c + 1, 2c + 8, 2c + 9
+    auto load_k = [&](long long row, int valid) {
+        const bf16* k = p.k + row * D + c * 8;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                kk[t][i] = few_load(k + (g + 8 * t) * D + i * 32, g + 8 * t < valid);
+    };
+    auto load_v = [&](long long row, int valid) {
+        const bf16* v = p.v + row * D + g * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int key = 2 * c + (j & 1) + (j >> 1) * 8;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+                vv[j][h] = few_load(v + key * D + h * 64, key < valid);
+        }
+    };
+
+    float o[kHalves * 8][4];
+#pragma unroll
+    for (int t = 0; t < kHalves * 8; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+    float m0 = kFewEmpty, m1 = kFewEmpty, l0 = 0.f, l1 = 0.f;   // rows g, g + 8
+
+    const int u_end = min(2 * st.n_sel, (split + 1) * p.per);
+    int u = split * p.per;
+    long long row = 0;
+    int valid = 0;
+    if (u < u_end) {
+        locate(u, &row, &valid);
+        load_k(row, valid);
+        load_v(row, valid);
+    }
+    while (u < u_end) {
+        const int now = valid;
+        float s[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                mma16816(s[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kk[t][i].x, kk[t][i].y);
+                mma16816(s[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kk[t][i].z, kk[t][i].w);
+            }
+        }
+        if (++u < u_end) {      // the next keys, while this strip's softmax runs
+            locate(u, &row, &valid);
+            load_k(row, valid);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[t][i] = 8 * t + 2 * c + (i & 1) < now ? s[t][i] * p.scale_log2 : -INFINITY;
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+        }
+        // the maximum moves only when it grows by more than 8 (log2 units):
+        // P stays below 2^8 and O is seldom rescaled
+        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float a0 = few_ex2(m0 - n0), a1 = few_ex2(m1 - n1);
+            m0 = n0, m1 = n1;
+            l0 *= a0, l1 *= a1;
+#pragma unroll
+            for (int t = 0; t < kHalves * 8; ++t) {
+                o[t][0] *= a0, o[t][1] *= a0;
+                o[t][2] *= a1, o[t][3] *= a1;
+            }
+        }
+        // P rounded to nearest bf16, its sum over the unrounded values
+        uint32_t pa[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float e0 = few_ex2(s[t][0] - m0), e1 = few_ex2(s[t][1] - m0);
+            const float e2 = few_ex2(s[t][2] - m1), e3 = few_ex2(s[t][3] - m1);
+            l0 += e0 + e1;
+            l1 += e2 + e3;
+            pa[2 * t] = few_pack(e0, e1);
+            pa[2 * t + 1] = few_pack(e2, e3);
+        }
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vv[0][h]);
+            const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vv[1][h]);
+            const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vv[2][h]);
+            const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vv[3][h]);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const uint32_t sel = t & 1 ? 0x7632u : 0x5410u;
+                mma16816(o[h * 8 + t], pa[0], pa[1], pa[2], pa[3],
+                         __byte_perm(v0[t / 2], v1[t / 2], sel),
+                         __byte_perm(v2[t / 2], v3[t / 2], sel));
+            }
+        }
+        if (u < u_end) load_v(row, valid);
+    }
+
+    // the warps' results
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    if (c == 0) {
+        sh.m[warp][g] = m0, sh.m[warp][g + 8] = m1;
+        sh.l[warp][g] = l0, sh.l[warp][g + 8] = l1;
+    }
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = g + (i >> 1) * 8;
+            if (r < rows) {
+                float4* d4 = reinterpret_cast<float4*>(&sh.o[warp][r][h * 64 + c * 16 + (i & 1) * 8]);
+                d4[0] = make_float4(o[h * 8][i], o[h * 8 + 1][i], o[h * 8 + 2][i], o[h * 8 + 3][i]);
+                d4[1] = make_float4(o[h * 8 + 4][i], o[h * 8 + 5][i], o[h * 8 + 6][i], o[h * 8 + 7][i]);
+            }
+        }
+    __syncthreads();
+    const float ln2 = 0.69314718055994531f;
+    const size_t slot_f = few_slot_floats(D);
+    float* mine = p.partial + blockIdx.x * slot_f;
+    constexpr int kRowStep = kFewThreads / D;      // rows that the CTA joins at a time
+    const int d = threadIdx.x % D;
+    auto put = [&](int r, float acc, float M, float L) {
+        const bool none = !(L > 0.f) && !isnan(L);   // a row without keys: 0 and -inf
+        const size_t tok = (size_t)st.out_tok0 + row0 + r;
+        p.out[(tok * p.heads + head) * D + d] = __float2bfloat16_rn(none ? 0.f : acc / L);
+        if (d == 0 && p.lse)
+            p.lse[tok * p.heads + head] = none ? -INFINITY : (M + __log2f(L)) * ln2;
+    };
+    for (int r = threadIdx.x / D; r < rows; r += kRowStep) {
+        float M = sh.m[0][r], L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 1; w < kFewWarps; ++w) M = fmaxf(M, sh.m[w][r]);
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+            const float a = few_ex2(sh.m[w][r] - M);
+            L = fmaf(a, sh.l[w][r], L);
+            acc = fmaf(a, sh.o[w][r][d], acc);
+        }
+        if (st.splits == 1) {
+            put(r, acc, M, L);
+        } else {
+            __stcg(mine + r * D + d, acc);
+            if (d == 0) {
+                __stcg(mine + kFewRows * D + r, M);
+                __stcg(mine + kFewRows * D + kFewRows + r, L);
+            }
+        }
+    }
+    if (st.splits == 1) return;
+    __threadfence();     // this CTA's part is visible before its arrival
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int* cnt = p.counters + st.item0 + item;
+        const int last = atomicAdd(cnt, 1) == st.splits - 1;
+        if (last) *cnt = 0;    // ready for the next launch
+        sh.last = last;
+    }
+    __syncthreads();
+    if (!sh.last) return;
+    __threadfence();
+    const float* parts = p.partial + (size_t)(blockIdx.x - split) * slot_f;
+    for (int r = threadIdx.x / D; r < rows; r += kRowStep) {
+        float M = kFewEmpty, L = 0.f, acc = 0.f;
+        for (int k0 = 0; k0 < st.splits; k0 += 8) {
+            float mk[8], lk[8], ok[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool in = k0 + k < st.splits;
+                const float* pk = parts + (size_t)(k0 + k) * slot_f;
+                mk[k] = in ? __ldcg(pk + kFewRows * D + r) : kFewEmpty;
+                lk[k] = in ? __ldcg(pk + kFewRows * D + kFewRows + r) : 0.f;
+                ok[k] = in ? __ldcg(pk + r * D + d) : 0.f;
+            }
+            float Mn = M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) Mn = fmaxf(Mn, mk[k]);
+            const float a = few_ex2(M - Mn);
+            L *= a, acc *= a;
+            M = Mn;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = few_ex2(mk[k] - M);
+                L = fmaf(w, lk[k], L);
+                acc = fmaf(w, ok[k], acc);
+            }
+        }
+        put(r, acc, M, L);
+    }
+}
+
+template <typename Pages>
+cudaError_t launch_few_any(const FewArgs<Pages>& a, int head_dim, int ctas, cudaStream_t s) {
+    if (head_dim == 128)
+        few_kernel<128, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+    else
+        few_kernel<64, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+static_assert(sizeof(FewArgs<PageTable>) <= 32000, "kernel parameters too large");
+
+}  // namespace
+
+cudaError_t launch_few(const FewArgs<FixedRows>& a, int head_dim, int ctas, cudaStream_t s) {
+    return launch_few_any(a, head_dim, ctas, s);
+}
+cudaError_t launch_few(const FewArgs<PageTable>& a, int head_dim, int ctas, cudaStream_t s) {
+    return launch_few_any(a, head_dim, ctas, s);
+}
+
+bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, size_t part_floats,
+              int n_counters, int* per, int* ctas) {
+    long long units = 0;
+    for (int i = 0; i < n_streams; ++i)
+        units += (long long)heads * ((st[i].n_q + kFewRows - 1) / kFewRows) * 2 * st[i].n_sel;
+    // one wave of resident CTAs (by registers: two to an SM for 128-wide
+    // heads, four for 64-wide ones)
+    const long long wave = (long long)n_sm * (head_dim == 128 ? 2 : 4);
+    const long long p = std::max(1LL, (units + wave - 1) / wave);
+    long long cta = 0, item = 0;
+    for (int i = 0; i < n_streams; ++i) {
+        FewStream& s = st[i];
+        const long long items = (long long)heads * ((s.n_q + kFewRows - 1) / kFewRows);
+        s.splits = (int)((2LL * s.n_sel + p - 1) / p);
+        s.cta0 = (int)cta;
+        s.item0 = (int)item;
+        cta += items * s.splits;
+        item += items;
+        if (cta >= (1LL << 31) || item > n_counters) return false;
+    }
+    if ((size_t)cta * few_slot_floats(head_dim) > part_floats || p > (1 << 30)) return false;
+    *per = (int)p;
+    *ctas = (int)cta;
+    return true;
+}
+
+}  // namespace pv

@@ -146,10 +146,19 @@ def _dense(t) -> int | None:
     return _ptr(t)
 
 
+_current = None  # (current device, raw stream of a device), once CUDA has been seen
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _current
+        if _current is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            _current = (torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+        device, raw = _current
+        return raw(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -469,11 +478,13 @@ class KVStore:
         self.handle = pv_kv_init(cfg, *bufs) if pages is None else pv_kv_init_paged(cfg, pages, *bufs)
         self.T = cfg.frame_w * cfg.frame_h
         self.ltot = (cfg.first_frames + cfg.ring_slots if pages is None else pages) * self.T
-        self.summ_buf = None
+        self.summ_buf = self._summ = None
         if summaries:
             n = pv_kv_summary_bytes(self.handle)
             self.summ_buf = torch.empty(n, dtype=torch.uint8, device=device)
             pv_kv_set_summaries(self.handle, self.summ_buf, n)
+            rows = self.ltot // self.T * -(-self.T // PV_BLOCK_KEYS)
+            self._summ = self.summ_buf.view(torch.float32).view(self._shape(rows))
 
     def _shape(self, rows):
         """[layers][steps][streams][heads][rows][D], without streams for a paged store."""
@@ -495,9 +506,7 @@ class KVStore:
 
     def summary_region(self):
         """The block means as f32, like k_region with ceil(T / 128) rows per frame (a view)."""
-        import torch
-        rows = self.ltot // self.T * -(-self.T // PV_BLOCK_KEYS)
-        return self.summ_buf.view(torch.float32).view(self._shape(rows))
+        return self._summ
 
     def close(self):
         if self.handle:

@@ -328,7 +328,7 @@ SHAPE, ARG, CAP = pv.PV_ERR_SHAPE, pv.PV_ERR_INVALID_ARG, pv.PV_ERR_CAPACITY
     ((None, 5, 1, 64, 16), ARG), ((16, 5, 1, 64, None), ARG), ((8, 5, 1, 64, 16), ARG),
     ((16, 5, 1, 64, 8), ARG), ((16, 0, 1, 64, 16), SHAPE), ((16, 5, 0, 64, 16), SHAPE),
     ((16, 5, 1, 96, 16), SHAPE), ((16, (1 << 30) + 1, 1, 64, 16), SHAPE),
-    ((16, 1 << 20, 2048, 64, 16), SHAPE), ((16, 1, 65536, 64, 16), SHAPE)])
+    ((16, 1 << 20, 2048, 64, 16), SHAPE)])
 def test_summarize_dense_refusals(args, status):
     with pytest.raises(pv.PVError) as e:
         pv.pv_block_summarize_dense(*args, cuda_stream=0)
