@@ -1090,7 +1090,7 @@ pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, c
             return e == cudaSuccess ? PV_OK : cuda_fail(e, "block attention launch");
         }
     }
-    if (plan_attention(p, c.n_sm, c.n_partials, c.n_counters) < 0)
+    if (plan_attention(p, c.n_sm, c.n_partials, c.n_counters, true) < 0)
         return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
     BlockArgs<Pages> b{};
     b.list = c.list;

@@ -766,7 +766,7 @@ __device__ __forceinline__ void l2_discard(const float* a, float after) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(a), "f"(after) : "memory");
 }
 
-template <int D, bool kBlocks>
+template <int D>
 __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, int X, int r,
                                             bool row_ok, bool keep, uint32_t tO, float m_own,
                                             float l_own, bf16* dst, float* lse_dst,
@@ -797,9 +797,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, i
             }
         }
     }
-    // listed blocks may leave a row without keys: it gives 0 and -inf
-    const bool none = kBlocks && !(L > 0.f);
-    const float invL = none ? 0.f : 1.0f / L;
+    const float invL = 1.0f / L;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         float acc[32];
@@ -832,8 +830,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Seg& g, i
             store_row32(dst + c, o, 1.0f);
         }
     }
-    if (row_ok && lse_dst)
-        *lse_dst = none ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+    if (row_ok && lse_dst) *lse_dst = (M + __log2f(L)) * 0.69314718055994531f;
     // every part's lines of this warp's 32 rows (the merging CTA's own part
     // too: it was written before the arrival count and read from TMEM): a
     // line per lane and 32 columns, then the m and l lines
@@ -953,8 +950,8 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
         // On the CTA's last segment O may stay in TMEM until the arrival
         // count says whether this CTA merges: the merge then reads its own
         // part from there instead of back from global memory.
-        const bool keep = !whole && it.pos >= it.end;
-        const bool none = B::kBlocks && !(l > 0.f);  // a row without keys: 0 and -inf
+        const bool keep = !B::kBlocks && !whole && it.pos >= it.end;
+        const bool none = B::kBlocks && l == 0.f;  // a row without keys: 0 and -inf
         const float inv = none ? 0.f : 1.0f / l;
         bf16* dst = p.out + ((size_t)tok * p.heads + g.head) * D;
         float* mine = p.partial + part_slot(p, blockIdx.x, g.i0, X) * slot_f;
@@ -976,7 +973,7 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
                 } else if (row_ok) {
                     store_row32(dst + c, o, inv);
                 }
-            } else {
+            } else if (!B::kBlocks || wq * 32 < g.rows[X]) {
                 const unsigned long long pol = l2_keep_policy();
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -999,6 +996,7 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
             st_keep(mine + (size_t)kQRows * D + r, m, pol);
             st_keep(mine + (size_t)kQRows * D + kQRows + r, l, pol);
         }
+        if constexpr (B::kBlocks) continue;  // join_kernel merges the parts
         // all four warps' partial rows are visible before the arrival count
         // moves; bounded waits on mbarriers, not bar.sync, so that an
         // aborting CTA can never block here
@@ -1021,7 +1019,7 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
         ++ec;
         if (ok && b->last[X]) {
             fence_gpu();
-            merge_parts<D, B::kBlocks>(p, g, X, r, row_ok, keep, tO, m, l, dst,
+            merge_parts<D>(p, g, X, r, row_ok, keep, tO, m, l, dst,
                            p.lse ? p.lse + (size_t)tok * p.heads + g.head : nullptr, to, ebuf,
                            warp_full, tok_w);
         }
@@ -1034,6 +1032,56 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
     // this warp's output stores are complete before the CTA ends
     if ((threadIdx.x & 31) == 0) bulk_wait_all();
     __syncwarp();
+}
+
+// Merge of the split items of a launch over listed blocks, as a launch of its
+// own: with few items an item has many parts, and one CTA reading them all
+// took most of the time (4 heads, 128 queries, 32 blocks: 95 us, against 19
+// with this).  One CTA per (item, query tile, 32 columns), a thread per row,
+// parts in order; bound by latency.
+constexpr int kJoinCols = 32;
+template <int D>
+__global__ void __launch_bounds__(kQRows) join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kChunks = D / kJoinCols;
+    const int c0 = (int)(blockIdx.x % kChunks) * kJoinCols;
+    const int X = (int)(blockIdx.x / kChunks) & 1;
+    const int item = (int)(blockIdx.x / (2 * kChunks));
+    Seg g;
+    item_seg<true>(p, item, g);
+    const AttnStreamDesc& s = p.st[g.si];
+    const int first = cta_of(p, g.i0);
+    const int nseg = cta_of(p, g.i0 + s.n_kt - 1) - first + 1;
+    const int r = threadIdx.x;
+    if (nseg == 1 || r >= g.rows[X]) return;
+    const size_t slot_f = partial_slot_floats(D);
+    auto part = [&](int k) { return p.partial + part_slot(p, first + k, g.i0, X) * slot_f; };
+    float M = kEmptyMax, L = 0.f, acc[kJoinCols];
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i) acc[i] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < nseg; ++k) {
+        const float* pk = part(k);
+        const float m = __ldcg(pk + (size_t)kQRows * D + r);
+        const float l = __ldcg(pk + (size_t)kQRows * D + kQRows + r);
+        float o[kJoinCols];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) o[i] = __ldcg(pk + (size_t)(c0 + i) * kQRows + r);
+        const float Mn = fmaxf(M, m);
+        const float a = ex2(M - Mn), w = ex2(m - Mn);
+        M = Mn;
+        L = fmaf(L, a, w * l);
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) acc[i] = fmaf(acc[i], a, w * o[i]);
+    }
+    const bool none = L == 0.f;  // a row without keys: 0 and -inf
+    const float inv = none ? 0.f : 1.0f / L;
+    const size_t tok = (size_t)s.out_tok0 + g.q0 + X * kQRows + r;
+    uint32_t o[kJoinCols];
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i) o[i] = __float_as_uint(acc[i]);
+    store_row32(p.out + (tok * p.heads + g.head) * D + c0, o, inv);
+    if (c0 == 0 && p.lse)
+        p.lse[tok * p.heads + g.head] = none ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 // kRun: whole items handed out at run time (AttnParams::item_aligned == 1);
@@ -1124,6 +1172,11 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
     const cudaError_t e = smem_limit_once(attn_kernel<D, kRun, B>, C::kSmem, configured);
     if (e != cudaSuccess) return e;
     attn_kernel<D, kRun, B><<<p.grid, kThreads, C::kSmem, s>>>(tq, tk, tv, to, p, ba);
+    if (B::kBlocks && !kRun) {
+        const cudaError_t e2 = cudaGetLastError();
+        if (e2 != cudaSuccess) return e2;
+        join_kernel<D><<<(unsigned)p.n_items * 2 * (D / kJoinCols), kQRows, 0, s>>>(p);
+    }
     return cudaGetLastError();
 }
 

@@ -57,12 +57,6 @@ struct FewShared {
     int last;
 };
 
-// One row of an item from its parts' (m, l, o): acc = sum_i 2^(m_i - M) o_i,
-// L = sum_i 2^(m_i - M) l_i.
-struct FewRow {
-    float M, L;
-};
-
 template <int D, typename Pages>
 __global__ void __launch_bounds__(kFewThreads)
     few_kernel(const __grid_constant__ FewArgs<Pages> p) {
@@ -99,8 +93,9 @@ __global__ void __launch_bounds__(kFewThreads)
     // unit u: keys [64 (u % 2), + 64) of listed block u / 2; this warp's 16
     // keys from row 16 warp on.  Rows of the block's first key, valid keys.
     const long long base = (long long)p.kb.seg0[si] + (long long)head * p.kb.head_segs;
-    auto locate = [&](int u, long long* row, int* valid) {
-        const int b = list ? __ldg(list + u / 2) : u / 2;
+    const int u_end = min(2 * st.n_sel, (split + 1) * p.per);
+    auto entry = [&](int u) { return u >= u_end ? -1 : list ? __ldg(list + u / 2) : u / 2; };
+    auto locate = [&](int u, int b, long long* row, int* valid) {
         const int k0 = (u % 2) * kFewUnit + warp * 16;
         *row = 0;
         *valid = 0;
@@ -110,7 +105,8 @@ __global__ void __launch_bounds__(kFewThreads)
         *row = (base + p.pages.page(p.kb, si, seg)) * p.kb.seg_len + blk * kKeyTile + k0;
     };
     uint4 kk[2][kPieces];       // keys g and g + 8 of the strip
-    uint4 vv[4][kHalves];       // values of keys 2c, 2c + 1, 2c + 8, 2c + 9
+    // values of keys 2c, 2c + 1, 2c + 8, 2c + 9, of this strip and the next
+    uint4 vv[4][kHalves], vn[4][kHalves];
     auto load_k = [&](long long row, int valid) {
         const bf16* k = p.k + row * D + c * 8;
 #pragma unroll
@@ -119,14 +115,14 @@ __global__ void __launch_bounds__(kFewThreads)
             for (int i = 0; i < kPieces; ++i)
                 kk[t][i] = few_load(k + (g + 8 * t) * D + i * 32, g + 8 * t < valid);
     };
-    auto load_v = [&](long long row, int valid) {
+    auto load_v = [&](uint4 (&dst)[4][kHalves], long long row, int valid) {
         const bf16* v = p.v + row * D + g * 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int key = 2 * c + (j & 1) + (j >> 1) * 8;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
-                vv[j][h] = few_load(v + key * D + h * 64, key < valid);
+                dst[j][h] = few_load(v + key * D + h * 64, key < valid);
         }
     };
 
@@ -137,14 +133,15 @@ __global__ void __launch_bounds__(kFewThreads)
         for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     float m0 = kFewEmpty, m1 = kFewEmpty, l0 = 0.f, l1 = 0.f;   // rows g, g + 8
 
-    const int u_end = min(2 * st.n_sel, (split + 1) * p.per);
     int u = split * p.per;
     long long row = 0;
     int valid = 0;
+    int next_b = entry(u);      // list entries are read one unit ahead of their use
     if (u < u_end) {
-        locate(u, &row, &valid);
+        locate(u, next_b, &row, &valid);
         load_k(row, valid);
-        load_v(row, valid);
+        load_v(vv, row, valid);
+        next_b = entry(u + 1);
     }
     while (u < u_end) {
         const int now = valid;
@@ -159,9 +156,11 @@ __global__ void __launch_bounds__(kFewThreads)
                 mma16816(s[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kk[t][i].z, kk[t][i].w);
             }
         }
-        if (++u < u_end) {      // the next keys, while this strip's softmax runs
-            locate(u, &row, &valid);
+        if (++u < u_end) {      // the next strip, while this one is worked on
+            locate(u, next_b, &row, &valid);
             load_k(row, valid);
+            load_v(vn, row, valid);
+            next_b = entry(u + 1);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -213,7 +212,10 @@ __global__ void __launch_bounds__(kFewThreads)
                          __byte_perm(v2[t / 2], v3[t / 2], sel));
             }
         }
-        if (u < u_end) load_v(row, valid);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) vv[j][h] = vn[j][h];
     }
 
     // the warps' results
@@ -241,29 +243,38 @@ __global__ void __launch_bounds__(kFewThreads)
     const float ln2 = 0.69314718055994531f;
     const size_t slot_f = few_slot_floats(D);
     float* mine = p.partial + blockIdx.x * slot_f;
-    constexpr int kRowStep = kFewThreads / D;      // rows that the CTA joins at a time
-    const int d = threadIdx.x % D;
-    auto put = [&](int r, float acc, float M, float L) {
-        const bool none = !(L > 0.f) && !isnan(L);   // a row without keys: 0 and -inf
+    // joins: four columns of a row to a thread
+    constexpr int kCols = D / 4;
+    constexpr int kRowStep = kFewThreads / kCols;
+    const int d = threadIdx.x % kCols * 4;
+    auto put = [&](int r, const float4& acc, float M, float L) {
+        const bool none = L == 0.f;   // a row without keys: 0 and -inf
+        const float inv = none ? 0.f : 1.0f / L;
         const size_t tok = (size_t)st.out_tok0 + row0 + r;
-        p.out[(tok * p.heads + head) * D + d] = __float2bfloat16_rn(none ? 0.f : acc / L);
+        *reinterpret_cast<uint2*>(p.out + (tok * p.heads + head) * D + d) =
+            make_uint2(few_pack(acc.x * inv, acc.y * inv), few_pack(acc.z * inv, acc.w * inv));
         if (d == 0 && p.lse)
             p.lse[tok * p.heads + head] = none ? -INFINITY : (M + __log2f(L)) * ln2;
     };
-    for (int r = threadIdx.x / D; r < rows; r += kRowStep) {
-        float M = sh.m[0][r], L = 0.f, acc = 0.f;
+    auto add = [](float4& acc, float w, const float4& v) {
+        acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+    };
+    for (int r = threadIdx.x / kCols; r < rows; r += kRowStep) {
+        float M = sh.m[0][r], L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 1; w < kFewWarps; ++w) M = fmaxf(M, sh.m[w][r]);
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
             const float a = few_ex2(sh.m[w][r] - M);
             L = fmaf(a, sh.l[w][r], L);
-            acc = fmaf(a, sh.o[w][r][d], acc);
+            add(acc, a, *reinterpret_cast<const float4*>(&sh.o[w][r][d]));
         }
         if (st.splits == 1) {
             put(r, acc, M, L);
         } else {
-            __stcg(mine + r * D + d, acc);
+            __stcg(reinterpret_cast<float4*>(mine + r * D + d), acc);
             if (d == 0) {
                 __stcg(mine + kFewRows * D + r, M);
                 __stcg(mine + kFewRows * D + kFewRows + r, L);
@@ -283,29 +294,34 @@ __global__ void __launch_bounds__(kFewThreads)
     if (!sh.last) return;
     __threadfence();
     const float* parts = p.partial + (size_t)(blockIdx.x - split) * slot_f;
-    for (int r = threadIdx.x / D; r < rows; r += kRowStep) {
-        float M = kFewEmpty, L = 0.f, acc = 0.f;
-        for (int k0 = 0; k0 < st.splits; k0 += 8) {
-            float mk[8], lk[8], ok[8];
+    for (int r = threadIdx.x / kCols; r < rows; r += kRowStep) {
+        float M = kFewEmpty, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 16;   // parts in flight
+        for (int k0 = 0; k0 < st.splits; k0 += kBatch) {
+            float mk[kBatch], lk[kBatch];
+            float4 ok[kBatch];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kBatch; ++k) {
                 const bool in = k0 + k < st.splits;
                 const float* pk = parts + (size_t)(k0 + k) * slot_f;
                 mk[k] = in ? __ldcg(pk + kFewRows * D + r) : kFewEmpty;
                 lk[k] = in ? __ldcg(pk + kFewRows * D + kFewRows + r) : 0.f;
-                ok[k] = in ? __ldcg(pk + r * D + d) : 0.f;
+                ok[k] = in ? __ldcg(reinterpret_cast<const float4*>(pk + r * D + d))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float Mn = M;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) Mn = fmaxf(Mn, mk[k]);
+            for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, mk[k]);
             const float a = few_ex2(M - Mn);
-            L *= a, acc *= a;
+            L *= a;
+            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
             M = Mn;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kBatch; ++k) {
                 const float w = few_ex2(mk[k] - M);
                 L = fmaf(w, lk[k], L);
-                acc = fmaf(w, ok[k], acc);
+                add(acc, w, ok[k]);
             }
         }
         put(r, acc, M, L);

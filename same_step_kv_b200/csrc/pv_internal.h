@@ -343,6 +343,8 @@ pv_status report_error(pv_status code, const char* msg);
 // at least two) do not fit.  Long items run stream-K; short items, or a
 // workspace without room for the partial slots (4 per CTA), get whole items
 // handed out at run time instead.
-int plan_attention(AttnParams& p, int n_sm, int part_capacity, int cnt_capacity);
+// blocks: a launch over listed blocks, whose split items a second launch joins.
+int plan_attention(AttnParams& p, int n_sm, int part_capacity, int cnt_capacity,
+                   bool blocks = false);
 
 }  // namespace pv

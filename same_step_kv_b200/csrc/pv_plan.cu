@@ -28,7 +28,29 @@
 
 namespace pv {
 
-int plan_attention(AttnParams& p, int n_sm, int part_capacity, int cnt_capacity) {
+namespace {
+// Listed blocks: whether equal shares of the key tiles (joined by a second
+// launch) beat whole items handed out.  In key-tile iterations: an item costs
+// its tiles and about 1.6 more; whole items end with the last round, or, when
+// their lengths differ, on average half an item late; the join costs about 3.
+// From eight rounds on the hand-out stays, whatever the last round loses: it
+// walks the heads in order, so that the keys of those at work stay in L2.
+bool shares_beat_items(const AttnParams& p, int max_kt, long long sms, long long grid_sk) {
+    const double item_cost = 1.6, join_cost = 3.0;
+    const long long items = p.n_items;
+    if (items >= 8 * sms) return false;
+    bool uniform = true;
+    for (int i = 0; i < p.n_streams; ++i)
+        uniform = uniform && (p.st[i].n_qb == 0 || p.st[i].n_kt == max_kt);
+    const double whole = uniform ? (double)((items + sms - 1) / sms) * (max_kt + item_cost)
+                                 : (double)p.total / sms + item_cost * items / sms + 0.5 * max_kt;
+    const double shares =
+        (double)p.total / grid_sk + item_cost * ((double)items / grid_sk + 1) + join_cost;
+    return shares < whole;
+}
+}  // namespace
+
+int plan_attention(AttnParams& p, int n_sm, int part_capacity, int cnt_capacity, bool blocks) {
     auto lay_out = [&]() {
         long long total = 0;
         int items = 0;
@@ -52,7 +74,8 @@ int plan_attention(AttnParams& p, int n_sm, int part_capacity, int cnt_capacity)
     if (std::max<long long>(items * kQTilesPerCta, 2) > cnt_capacity || total <= 0) return -1;
     const int sms = std::max(1, std::min(n_sm, kMaxGrid));
     const long long grid_sk = std::min<long long>(sms, total);
-    const bool short_items = total / grid_sk >= 2LL * max_kt;
+    const bool short_items =
+        blocks ? !shares_beat_items(p, max_kt, sms, grid_sk) : total / grid_sk >= 2LL * max_kt;
     if (4 * grid_sk <= part_capacity && !short_items) {
         p.item_aligned = 0;
         p.grid = (int)grid_sk;
