@@ -1036,50 +1036,63 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
 
 // Merge of the split items of a launch over listed blocks, as a launch of its
 // own: with few items an item has many parts, and one CTA reading them all
-// took most of the time (4 heads, 128 queries, 32 blocks: 95 us, against 19
-// with this).  One CTA per (item, query tile, 32 columns), a thread per row,
+// took most of the time (4 heads, 128 queries, 32 blocks: 95 us, against 18
+// with this).  One CTA per (item, query tile, 16 columns), a thread per row,
 // parts in order; bound by latency.
-constexpr int kJoinCols = 32;
+constexpr int kJoinCols = 16;
+constexpr int kJoinParts = 4;   // parts in flight
 template <int D>
 __global__ void __launch_bounds__(kQRows) join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kChunks = D / kJoinCols;
     const int c0 = (int)(blockIdx.x % kChunks) * kJoinCols;
     const int X = (int)(blockIdx.x / kChunks) & 1;
-    const int item = (int)(blockIdx.x / (2 * kChunks));
     Seg g;
-    item_seg<true>(p, item, g);
+    item_seg<true>(p, (int)(blockIdx.x / (2 * kChunks)), g);
     const AttnStreamDesc& s = p.st[g.si];
     const int first = cta_of(p, g.i0);
-    const int nseg = cta_of(p, g.i0 + s.n_kt - 1) - first + 1;
+    const int n = cta_of(p, g.i0 + s.n_kt - 1) - first + 1;
     const int r = threadIdx.x;
-    if (nseg == 1 || r >= g.rows[X]) return;
+    if (n == 1 || r >= g.rows[X]) return;
     const size_t slot_f = partial_slot_floats(D);
-    auto part = [&](int k) { return p.partial + part_slot(p, first + k, g.i0, X) * slot_f; };
+    // only the first CTA may have begun before the item
+    const size_t slot0 = part_slot(p, first, g.i0, X), slot1 = (size_t)(first + 1) * 4 + X;
     float M = kEmptyMax, L = 0.f, acc[kJoinCols];
 #pragma unroll
     for (int i = 0; i < kJoinCols; ++i) acc[i] = 0.f;
-#pragma unroll 2
-    for (int k = 0; k < nseg; ++k) {
-        const float* pk = part(k);
-        const float m = __ldcg(pk + (size_t)kQRows * D + r);
-        const float l = __ldcg(pk + (size_t)kQRows * D + kQRows + r);
-        float o[kJoinCols];
+    for (int k0 = 0; k0 < n; k0 += kJoinParts) {
+        float m[kJoinParts], l[kJoinParts], o[kJoinParts][kJoinCols];
 #pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) o[i] = __ldcg(pk + (size_t)(c0 + i) * kQRows + r);
-        const float Mn = fmaxf(M, m);
-        const float a = ex2(M - Mn), w = ex2(m - Mn);
-        M = Mn;
-        L = fmaf(L, a, w * l);
+        for (int u = 0; u < kJoinParts; ++u) {
+            const int k = k0 + u;
+            const bool in = k < n;
+            const float* pk =
+                p.partial + (k == 0 || !in ? slot0 : slot1 + (size_t)(k - 1) * 4) * slot_f;
+            m[u] = in ? __ldcg(pk + (size_t)kQRows * D + r) : kEmptyMax;
+            l[u] = in ? __ldcg(pk + (size_t)kQRows * D + kQRows + r) : 0.f;
 #pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) acc[i] = fmaf(acc[i], a, w * o[i]);
+            for (int i = 0; i < kJoinCols; ++i)
+                o[u][i] = in ? __ldcg(pk + (size_t)(c0 + i) * kQRows + r) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kJoinParts; ++u) {
+            const float Mn = fmaxf(M, m[u]);
+            const float a = ex2(M - Mn), w = ex2(m[u] - Mn);
+            M = Mn;
+            L = fmaf(L, a, w * l[u]);
+#pragma unroll
+            for (int i = 0; i < kJoinCols; ++i) acc[i] = fmaf(acc[i], a, w * o[u][i]);
+        }
     }
     const bool none = L == 0.f;  // a row without keys: 0 and -inf
     const float inv = none ? 0.f : 1.0f / L;
     const size_t tok = (size_t)s.out_tok0 + g.q0 + X * kQRows + r;
-    uint32_t o[kJoinCols];
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * p.heads + g.head) * D + c0);
 #pragma unroll
-    for (int i = 0; i < kJoinCols; ++i) o[i] = __float_as_uint(acc[i]);
-    store_row32(p.out + (tok * p.heads + g.head) * D + c0, o, inv);
+    for (int i = 0; i < kJoinCols; i += 8)
+        dst[i / 8] = make_uint4(pack_bf16(acc[i] * inv, acc[i + 1] * inv),
+                                pack_bf16(acc[i + 2] * inv, acc[i + 3] * inv),
+                                pack_bf16(acc[i + 4] * inv, acc[i + 5] * inv),
+                                pack_bf16(acc[i + 6] * inv, acc[i + 7] * inv));
     if (c0 == 0 && p.lse)
         p.lse[tok * p.heads + g.head] = none ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }

@@ -2,9 +2,9 @@
 // short query sets, where the 128-row tiles of the tcgen05 kernel would be
 // almost empty and reading K and V is all the time there is.
 //
-// An item is (stream, head, 16 queries).  Its keys are cut into parts of
-// `per` units of 64 keys, one CTA of four warps to a part, so that few items
-// fill the GPU; a warp takes 16 keys of each unit.  Keys and values go from
+// An item is (stream, head, 16 queries).  Its keys, in units of 64, are cut
+// into even parts, one CTA of four warps to a part, so that few items fill the
+// GPU; a warp takes 16 keys of each unit.  Keys and values go from
 // global memory straight into the operand registers of mma.sync.m16n8k16
 // (M = the 16 queries): nothing is staged, so nothing waits at a barrier
 // inside the key loop, and a warp has its next keys in flight while it
@@ -93,8 +93,20 @@ __global__ void __launch_bounds__(kFewThreads)
     // unit u: keys [64 (u % 2), + 64) of listed block u / 2; this warp's 16
     // keys from row 16 warp on.  Rows of the block's first key, valid keys.
     const long long base = (long long)p.kb.seg0[si] + (long long)head * p.kb.head_segs;
-    const int u_end = min(2 * st.n_sel, (split + 1) * p.per);
-    auto entry = [&](int u) { return u >= u_end ? -1 : list ? __ldg(list + u / 2) : u / 2; };
+    const int units = 2 * st.n_sel;
+    const int u_end = (int)((split + 1LL) * units / st.splits);
+    // list entries: 32 blocks from block0 on and the 32 behind them, one to a lane
+    int u = (int)((long long)split * units / st.splits);
+    int block0 = u / 2;
+    auto fetch = [&](int b) {
+        b += lane;
+        return b >= st.n_sel ? -1 : list ? __ldg(list + b) : b;
+    };
+    int near = fetch(block0), far = fetch(block0 + 32);
+    auto entry = [&](int u) {
+        const int i = u / 2 - block0;
+        return __shfl_sync(0xffffffffu, i < 32 ? near : far, i & 31);
+    };
     auto locate = [&](int u, int b, long long* row, int* valid) {
         const int k0 = (u % 2) * kFewUnit + warp * 16;
         *row = 0;
@@ -133,15 +145,12 @@ __global__ void __launch_bounds__(kFewThreads)
         for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     float m0 = kFewEmpty, m1 = kFewEmpty, l0 = 0.f, l1 = 0.f;   // rows g, g + 8
 
-    int u = split * p.per;
     long long row = 0;
     int valid = 0;
-    int next_b = entry(u);      // list entries are read one unit ahead of their use
     if (u < u_end) {
-        locate(u, next_b, &row, &valid);
+        locate(u, entry(u), &row, &valid);
         load_k(row, valid);
         load_v(vv, row, valid);
-        next_b = entry(u + 1);
     }
     while (u < u_end) {
         const int now = valid;
@@ -157,10 +166,14 @@ __global__ void __launch_bounds__(kFewThreads)
             }
         }
         if (++u < u_end) {      // the next strip, while this one is worked on
-            locate(u, next_b, &row, &valid);
+            if (u / 2 - block0 == 32) {
+                block0 += 32;
+                near = far;
+                far = fetch(block0 + 32);
+            }
+            locate(u, entry(u), &row, &valid);
             load_k(row, valid);
             load_v(vn, row, valid);
-            next_b = entry(u + 1);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -349,27 +362,26 @@ cudaError_t launch_few(const FewArgs<PageTable>& a, int head_dim, int ctas, cuda
 }
 
 bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, size_t part_floats,
-              int n_counters, int* per, int* ctas) {
+              int n_counters, int* ctas) {
     long long units = 0;
     for (int i = 0; i < n_streams; ++i)
         units += (long long)heads * ((st[i].n_q + kFewRows - 1) / kFewRows) * 2 * st[i].n_sel;
     // one wave of resident CTAs (by registers: two to an SM for 128-wide
-    // heads, four for 64-wide ones)
+    // heads, four for 64-wide ones), shared out by keys
     const long long wave = (long long)n_sm * (head_dim == 128 ? 2 : 4);
-    const long long p = std::max(1LL, (units + wave - 1) / wave);
+    const long long per = std::max(1LL, (units + wave - 1) / wave);
     long long cta = 0, item = 0;
     for (int i = 0; i < n_streams; ++i) {
         FewStream& s = st[i];
         const long long items = (long long)heads * ((s.n_q + kFewRows - 1) / kFewRows);
-        s.splits = (int)((2LL * s.n_sel + p - 1) / p);
+        s.splits = (int)((2LL * s.n_sel + per - 1) / per);
         s.cta0 = (int)cta;
         s.item0 = (int)item;
         cta += items * s.splits;
         item += items;
         if (cta >= (1LL << 31) || item > n_counters) return false;
     }
-    if ((size_t)cta * few_slot_floats(head_dim) > part_floats || p > (1 << 30)) return false;
-    *per = (int)p;
+    if ((size_t)cta * few_slot_floats(head_dim) > part_floats) return false;
     *ctas = (int)cta;
     return true;
 }

@@ -170,14 +170,11 @@ cudaError_t launch_block_attn(const CUtensorMap& tq, const CUtensorMap& tk, cons
                               const CUtensorMap& to, const AttnParams& p,
                               const BlockArgs<PageTable>& b, cudaStream_t s);
 // Attention of few queries over listed blocks (pv_few.cu): items (stream,
-// head, 16 queries), each cut into `splits` parts of `per` units of 64 keys.
+// head, 16 queries), each cut into `splits` even parts of its units of 64 keys.
 constexpr int kFewRows = 16;
 constexpr int kFewUnit = 64;
 // Most queries of a stream that the kernel is used for.
-#ifndef PV_FEWQ
-#define PV_FEWQ 32
-#endif
-constexpr int kFewQueries = PV_FEWQ;
+constexpr int kFewQueries = 32;
 struct FewStream {
     int n_q, q_row0, out_tok0;
     int n_sel;           // listed blocks
@@ -193,7 +190,7 @@ struct FewArgs {
     float* lse;
     float* partial;      // few_slot_floats per CTA
     int* counters;       // arrivals per item; the last arriver resets to 0
-    int heads, per, n_streams;
+    int heads, n_streams;
     float scale_log2;
     const int* list;     // NULL: blocks 0 .. n_sel - 1
     int keep;
@@ -203,10 +200,10 @@ struct FewArgs {
     Pages pages;
 };
 __host__ __device__ inline size_t few_slot_floats(int D) { return (size_t)kFewRows * D + 2 * kFewRows; }
-// Lays out a.st (n_q and n_sel set; per, splits, cta0, item0 filled in) on
+// Lays out the streams (n_q and n_sel set; splits, cta0, item0 filled in) on
 // n_sm SMs.  False when the parts or counters do not fit.
 bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, size_t part_floats,
-              int n_counters, int* per, int* ctas);
+              int n_counters, int* ctas);
 cudaError_t launch_few(const FewArgs<FixedRows>& a, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_few(const FewArgs<PageTable>& a, int head_dim, int ctas, cudaStream_t s);
 // K or V rows as segments: a box is 128 rows x 64 columns of one segment,
