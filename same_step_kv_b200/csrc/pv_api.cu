@@ -1070,7 +1070,7 @@ pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, c
         }
         int ctas = 0;
         if (plan_few(f.st, p.n_streams, p.heads, p.head_dim, c.n_sm, c.part_floats, c.n_counters,
-                     &ctas)) {
+                     &f.rows, &ctas)) {
             f.q = (const bf16*)c.q;
             f.k = (const bf16*)c.k;
             f.v = (const bf16*)c.v;

@@ -471,7 +471,7 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUt
                 const int blk = max(next_b, 0);
                 const bool empty = next_b < 0;
                 next_b = br.at(j + 1);  // one tile ahead of its use
-                const int seg = blk / ba.kb.bps;
+                const int seg = segment_of(ba.kb, blk);
                 // an empty block lies past its segment's end: it reads as zeros
                 brow = (empty ? ba.kb.bps : blk - seg * ba.kb.bps) * kKeyTile;
                 bseg = ba.kb.seg0[s.id] + g.head * ba.kb.head_segs + ba.pages.page(ba.kb, s.id, seg);

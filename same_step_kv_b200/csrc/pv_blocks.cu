@@ -12,15 +12,6 @@
 #include <cooperative_groups.h>
 
 #include "pv_internal.h"
-#ifndef PV_LB
-#define PV_LB 3
-#endif
-#ifndef PV_SLB
-#define PV_SLB 3
-#endif
-#ifndef PV_QS
-#define PV_QS 0
-#endif
 
 namespace cg = cooperative_groups;
 
@@ -30,43 +21,13 @@ namespace {
 constexpr int kPoolThreads = 256;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
-__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-
-// Adds rows x and y (eight bf16 columns each) to f64 sums.  The conversions
-// to f64 share a slow pipe, so two values are added in f32 first and converted
-// once, wherever that addition is exact: s = x + y is, when both s - x == y
-// and s - y == x (of the two, the difference with the larger operand is
-// exact in f32, and equal to the other operand only if nothing was lost).
-// For values within about 16 binades of one another it always is.
-__device__ __forceinline__ void add_rows(double* a, const uint4& x4, const uint4& y4) {
-    const uint32_t xs[4] = {x4.x, x4.y, x4.z, x4.w}, ys[4] = {y4.x, y4.y, y4.z, y4.w};
-    const float2 neg = make_float2(-1.f, -1.f);
-    float2 s[4];
-    uint32_t lost = 0;
+// Adds a row (eight bf16 columns) to f64 sums.
+__device__ __forceinline__ void add_row(double* a, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 x = bf16_pair(xs[i]), y = bf16_pair(ys[i]);
-        s[i] = __fadd2_rn(x, y);
-        const float2 d = __ffma2_rn(y, neg, __ffma2_rn(x, neg, s[i]));
-        const float2 e = __ffma2_rn(x, neg, __ffma2_rn(y, neg, s[i]));
-        lost |= __float_as_uint(d.x) | __float_as_uint(e.x);
-        lost |= __float_as_uint(d.y) | __float_as_uint(e.y);
-    }
-    if (lost == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[2 * i] += (double)s[i].x;
-            a[2 * i + 1] += (double)s[i].y;
-        }
-    } else {  // also sums beyond f32, infinities and NaN
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = bf16_pair(xs[i]), y = bf16_pair(ys[i]);
-            a[2 * i] = a[2 * i] + (double)x.x + (double)y.x;
-            a[2 * i + 1] = a[2 * i + 1] + (double)x.y + (double)y.y;
-        }
+        a[2 * i] += (double)__uint_as_float(w[i] << 16);
+        a[2 * i + 1] += (double)__uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
 
@@ -81,15 +42,14 @@ __device__ __forceinline__ void pool_strip(const bf16* strip, int r0, int r1, do
     for (int c = 0; c < 8; ++c) a[c] = 0.0;
 #pragma unroll 1
     for (int r = r0 + lane / 8; r < r0 + kRows; r += 4 * kLoads) {
-        uint4 v[kLoads + kLoads % 2];
+        uint4 v[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             v[i] = r + 4 * i < r1
                        ? __ldg(reinterpret_cast<const uint4*>(strip + (size_t)(r + 4 * i) * D) + (lane & 7))
                        : make_uint4(0, 0, 0, 0);
-        if (kLoads % 2) v[kLoads] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kLoads; i += 2) add_rows(a, v[i], v[i + 1]);
+        for (int i = 0; i < kLoads; ++i) add_row(a, v[i]);
     }
 #pragma unroll
     for (int m = 8; m < 32; m *= 2)
@@ -101,7 +61,7 @@ __device__ __forceinline__ void pool_strip(const bf16* strip, int r0, int r1, do
 // one after the other, for few blocks.  One: long streams of loads without a
 // synchronisation, for many.  Bound by reading the keys.
 template <int D, int kParts>
-__global__ void __launch_bounds__(kPoolThreads, PV_SLB)
+__global__ void __launch_bounds__(kPoolThreads, 3)
     summary_kernel(const __grid_constant__ SummaryParams p) {
     constexpr int kStrips = D / 64;
     constexpr int kPer = kPoolWarps / (kStrips * kParts);    // blocks of a CTA
@@ -156,28 +116,45 @@ __global__ void __launch_bounds__(kPoolThreads, PV_SLB)
 // ------------------------------------------------------------------ select
 constexpr int kSelThreads = kPoolThreads;
 constexpr int kSelWarps = kPoolWarps;
-constexpr int kRankBlocks = 256;   // one block per thread: order by counting
+constexpr int kCountBlocks = 256;   // one block per thread: order by counting
+constexpr int kMaxClose = 512;      // blocks at the border that are scored again
+constexpr uint32_t kForced = 0xFFFFC000u;   // keys of forced blocks, above +inf's
 
-// f64 -> unsigned integer of the same order (-0 and +0 equal, NaN lowest).
+// Floating-point values as unsigned integers of the same order (-0 and +0
+// equal, NaN lowest).
 __device__ __forceinline__ unsigned long long order_key(double s) {
     if (!(s == s)) return 0;
     const long long b = __double_as_longlong(s + 0.0);
     return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ uint32_t order_key(float s) {
+    if (!(s == s)) return 0;
+    const uint32_t b = __float_as_uint(s + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
 struct SelShared {
     int warp_a[kSelWarps], warp_b[kSelWarps];
     int hist[256];
     int bin, need, all;
+    uint32_t edge;
+    uint32_t norm2;                     // largest |kmean|^2 (its bits)
+    int close[kMaxClose];               // blocks at the border
+    unsigned long long key[kMaxClose];  // and their f64 scores
 };
 
 // Threshold of the `need` largest of n keys (radix select, eight bits at a
 // time from the top): the keys whose upper bits exceed `prefix` are taken,
-// and of those that equal it all (*all) or the first *need.
-__device__ void radix_threshold(const unsigned long long* keys, int n, int need, SelShared* sh,
-                                int* shift_out, unsigned long long* prefix_out) {
-    unsigned long long prefix = 0;
-    int shift = 64;
+// and of those that equal it all (sh->all) or the first sh->need.
+template <typename K>
+__device__ void radix_threshold(const K* keys, int n, int need, SelShared* sh, int* shift_out,
+                                K* prefix_out) {
+    constexpr int kBits = sizeof(K) * 8;
+    K prefix = 0;
+    int shift = kBits;
     const int t = threadIdx.x;
     if (t == 0) {
         sh->need = need;
@@ -188,8 +165,8 @@ __device__ void radix_threshold(const unsigned long long* keys, int n, int need,
         sh->hist[t] = 0;
         __syncthreads();
         for (int i = t; i < n; i += kSelThreads) {
-            const unsigned long long k = keys[i] >> shift;
-            if (shift == 56 || (k >> 8) == prefix) atomicAdd(&sh->hist[(int)(k & 255)], 1);
+            const K k = keys[i] >> shift;
+            if (shift == kBits - 8 || (k >> 8) == prefix) atomicAdd(&sh->hist[(int)(k & 255)], 1);
         }
         __syncthreads();
         if (t < 32) {
@@ -215,11 +192,12 @@ __device__ void radix_threshold(const unsigned long long* keys, int n, int need,
             }
         }
         __syncthreads();
-        prefix = (prefix << 8) | (unsigned long long)sh->bin;
+        prefix = (prefix << 8) | (K)sh->bin;
         if (sh->all) break;
     }
     *shift_out = shift;
     *prefix_out = prefix;
+    __syncthreads();
 }
 
 // Position of this thread among the block's threads whose flag is set, and
@@ -241,59 +219,145 @@ __device__ __forceinline__ int block_rank(bool f, int* w, int* total) {
     return before + __popc(b & ((1u << lane) - 1));
 }
 
-// The n_sel largest of n keys, ties to the lowest index, as ascending
-// indices; -1 up to keep.
-__device__ void write_top(const unsigned long long* keys, int n, int n_sel, int keep, SelShared* sh,
-                          int* out) {
+// The need-th largest of n keys.
+__device__ uint32_t nth_key(const uint32_t* keys, int n, int need, SelShared* sh) {
     const int t = threadIdx.x;
-    if (n <= kRankBlocks) {
-        // every thread counts the keys ahead of its own: equal ones before it,
-        // larger ones anywhere (keys holds a 0 behind an odd n)
-        bool f = false;
+    if (n <= kCountBlocks) {
+        // the smallest key that fewer than `need` others exceed
+        uint32_t mine = 0xFFFFFFFFu;
         if (t < n) {
-            const unsigned long long k = keys[t];
-            const int w0 = t & ~31, w1 = min(n, w0 + 32);
-            const ulonglong2* two = reinterpret_cast<const ulonglong2*>(keys);
-            int ahead = 0;
+            const uint32_t k = keys[t];
+            const uint4* four = reinterpret_cast<const uint4*>(keys);   // zeros behind n
+            int above = 0;
 #pragma unroll 4
-            for (int i = 0; i < w0 / 2; ++i) {
-                const ulonglong2 o = two[i];
-                ahead += (o.x >= k) + (o.y >= k);
+            for (int i = 0; i < (n + 3) / 4; ++i) {
+                const uint4 o = four[i];
+                above += (o.x > k) + (o.y > k) + (o.z > k) + (o.w > k);
             }
-            for (int i = w0; i < w1; ++i) {
-                const unsigned long long o = keys[i];
-                ahead += o > k || (o == k && i < t);
-            }
-#pragma unroll 4
-            for (int i = (w1 + 1) / 2; i < (n + 1) / 2; ++i) {
-                const ulonglong2 o = two[i];
-                ahead += (o.x > k) + (o.y > k);
-            }
-            f = ahead < n_sel;
+            if (above < need) mine = k;
         }
-        int total;
-        const int pos = block_rank(f, sh->warp_a, &total);
-        if (f) out[pos] = t;
+        mine = __reduce_min_sync(0xffffffffu, mine);
+        if ((t & 31) == 0) atomicMin(&sh->edge, mine);
+        __syncthreads();
+        return sh->edge;
+    }
+    int shift;
+    uint32_t prefix;
+    radix_threshold(keys, n, need, sh, &shift, &prefix);
+    if (shift == 0) return prefix;
+    // every key of the last bin is among the `need`: the smallest of them
+    uint32_t mine = 0xFFFFFFFFu;
+    for (int i = t; i < n; i += kSelThreads)
+        if (keys[i] >> shift == prefix) mine = min(mine, keys[i]);
+    mine = __reduce_min_sync(0xffffffffu, mine);
+    if ((t & 31) == 0) atomicMin(&sh->edge, mine);
+    __syncthreads();
+    return sh->edge;
+}
+
+// Ascending indices of the n_sel largest of n f64 keys, ties to the lowest.
+__device__ void write_top(const unsigned long long* keys, int n, int n_sel, SelShared* sh, int* out) {
+    int shift;
+    unsigned long long prefix;
+    radix_threshold(keys, n, n_sel, sh, &shift, &prefix);
+    const bool all = sh->all != 0;
+    const int need = sh->need;
+    int base = 0, eq_base = 0;
+    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+        const int i = i0 + threadIdx.x;
+        const unsigned long long k = i < n ? keys[i] >> shift : 0;
+        const bool gt = i < n && k > prefix;
+        const bool eq = i < n && k == prefix;
+        int eqs, cnt;
+        const int er = eq_base + block_rank(eq, sh->warp_a, &eqs);
+        const bool f = gt || (eq && (all || er < need));
+        const int pos = base + block_rank(f, sh->warp_b, &cnt);
+        if (f) out[pos] = i;
+        base += cnt;
+        eq_base += eqs;
+    }
+}
+
+// The n_sel best of n blocks, as ascending indices; -1 up to keep.  keys
+// holds f32 scores, each off by at most `err`, on entry, f64 scores if they
+// are needed.  Blocks whose f32 score is more than 2 err above the n_sel-th
+// largest one are among the best whatever the errors, those more than 2 err
+// below are not, and the few between (seldom more than one) are scored in
+// f64 by score(b), eight lanes of a warp to a block.
+template <typename Score>
+__device__ void choose(unsigned long long* keys64, int n, int n_sel, int keep, float err,
+                       SelShared* sh, int* out, const Score& score) {
+    uint32_t* keys = reinterpret_cast<uint32_t*>(keys64);
+    const int t = threadIdx.x, sub = t / 8;   // 32 groups of eight lanes
+    const uint32_t edge = nth_key(keys, n, n_sel, sh);
+    // taken: keys from `above` on; close: keys from `from` up to it
+    uint32_t above, from;
+    if (edge >= kForced || edge == 0) {       // forced blocks alone; or NaN at the border
+        above = max(edge, 1u);
+        from = edge;
     } else {
-        int shift;
-        unsigned long long prefix;
-        radix_threshold(keys, n, n_sel, sh, &shift, &prefix);
-        const bool all = sh->all != 0;
-        const int need = sh->need;
-        int base = 0, eq_base = 0;
-        for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-            const int i = i0 + t;
-            const unsigned long long k = i < n ? keys[i] >> shift : 0;
-            const bool gt = i < n && k > prefix;
-            const bool eq = i < n && k == prefix;
-            int eqs, cnt;
-            const int er = eq_base + block_rank(eq, sh->warp_a, &eqs);
-            const bool f = gt || (eq && (all || er < need));
-            const int pos = base + block_rank(f, sh->warp_b, &cnt);
-            if (f) out[pos] = i;
-            base += cnt;
-            eq_base += eqs;
+        const float at = key_value(edge);
+        above = min(order_key(__fadd_ru(at, 2.f * err)), kForced - 1) + 1;
+        from = order_key(__fadd_rd(at, -2.f * err));
+        if (!(err < INFINITY)) above = kForced, from = 0;
+    }
+    int taken = 0, close = 0;
+    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+        const int i = i0 + t;
+        const uint32_t k = i < n ? keys[i] : 0;
+        const bool c = i < n && k >= from && k < above;
+        taken += __syncthreads_count(i < n && k >= above);
+        int cnt;
+        const int pos = close + block_rank(c, sh->warp_a, &cnt);
+        if (c && pos < kMaxClose) sh->close[pos] = i;
+        close += cnt;
+    }
+    __syncthreads();
+    if (taken + close > n_sel) {
+        if (close > kMaxClose) {
+            // too close to call (equal blocks, sums beyond f32): all in f64;
+            // forced blocks keep their rank
+            // (32 blocks at a time from the last one down: a block's f64 key
+            // covers f32 keys behind its own, which have been read)
+            for (int b0 = (n - 1) / 32 * 32; b0 >= 0; b0 -= 32) {
+                const int b = b0 + sub;
+                const uint32_t was = b < n ? keys[b] : 0;
+                const double s = score(min(b, n - 1));
+                __syncthreads();
+                if (b < n && (t & 7) == 0)
+                    keys64[b] = was >= kForced ? ~0ull : order_key(s);
+                __syncthreads();
+            }
+            write_top(keys64, n, n_sel, sh, out);
+            for (int i = n_sel + t; i < keep; i += kSelThreads) out[i] = -1;
+            return;
         }
+        for (int j0 = 0; j0 < close; j0 += 32) {
+            const int j = j0 + sub;
+            const double s = score(sh->close[min(j, close - 1)]);
+            if (j < close && (t & 7) == 0) sh->key[j] = order_key(s);
+        }
+        __syncthreads();
+        for (int j = t; j < close; j += kSelThreads) {
+            const unsigned long long k = sh->key[j];
+            int ahead = 0;
+            for (int i = 0; i < close; ++i) {
+                const unsigned long long o = sh->key[i];
+                ahead += o > k || (o == k && i < j);
+            }
+            keys[sh->close[j]] = ahead < n_sel - taken ? 0xFFFFFFFFu : 0u;
+        }
+        __syncthreads();
+        from = above;     // now marked
+    }
+    int base = 0;
+    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+        const int i = i0 + t;
+        const bool f = i < n && keys[i] >= from;
+        int cnt;
+        const int pos = base + block_rank(f, sh->warp_b, &cnt);
+        if (f) out[pos] = i;
+        base += cnt;
     }
     for (int i = n_sel + t; i < keep; i += kSelThreads) out[i] = -1;
 }
@@ -302,20 +366,24 @@ __device__ void write_top(const unsigned long long* keys, int n, int n_sel, int 
 // the group's rows (sums exchanged through distributed shared memory) and the
 // blocks to score; the first one picks the top.
 template <int D, int kCluster, typename Pages>
-__global__ void __launch_bounds__(kSelThreads, PV_LB)
+__global__ void __launch_bounds__(kSelThreads, 4)
     select_kernel(const __grid_constant__ SelectParams p, const __grid_constant__ Pages pages) {
     cg::cluster_group cl = cg::this_cluster();
     const int rank = kCluster > 1 ? (int)cl.block_rank() : 0;
-    extern __shared__ __align__(16) unsigned long long keys[];   // max_blocks, rounded up to even
+    extern __shared__ __align__(16) unsigned long long keys64[];   // max_blocks
     constexpr int kStrips = D / 64;
     constexpr int kParts = kSelWarps / kStrips;       // warps that share a strip's rows
     constexpr int kShare = kQBlock / kCluster;        // rows of a CTA
     __shared__ double part[kParts * D];
     __shared__ double mine[D];                        // this CTA's sums
-    __shared__ double qm[D];
+    __shared__ __align__(16) float qm[D];
     __shared__ SelShared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int item = blockIdx.x / kCluster;
+    if (threadIdx.x == 0) {
+        sh.norm2 = 0;
+        sh.edge = 0xFFFFFFFFu;
+    }
     int i = 0;
     while (i + 1 < p.n_streams && p.item0[i + 1] <= item) ++i;
     const int li = item - p.item0[i];
@@ -351,60 +419,93 @@ __global__ void __launch_bounds__(kSelThreads, PV_LB)
             for (int r = 0; r < kCluster; ++r) sum += cl.map_shared_rank(mine, r)[threadIdx.x];
         }
     }
-    if (threadIdx.x < D) qm[threadIdx.x] = (double)(float)(sum / (double)(q1 - q0));
+    if (threadIdx.x < D) qm[threadIdx.x] = (float)(sum / (double)(q1 - q0));
     __syncthreads();
 
-    // scores of this CTA's blocks, to the first CTA: eight lanes to a block,
-    // each with every eighth run of four columns
+    // f32 scores of this CTA's blocks, to the first CTA: eight lanes to a
+    // block, each with every eighth run of four columns
     constexpr int kRuns = D / 32;
     const int l8 = lane & 7;
-    double ql[kRuns][4];
+    float4 ql[kRuns];
 #pragma unroll
-    for (int c = 0; c < kRuns; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ql[c][k] = qm[(c * 8 + l8) * 4 + k];
-    unsigned long long* dst = kCluster > 1 ? cl.map_shared_rank(keys, 0) : keys;
+    for (int c = 0; c < kRuns; ++c) ql[c] = reinterpret_cast<const float4*>(qm)[c * 8 + l8];
+    uint32_t* keys = reinterpret_cast<uint32_t*>(keys64);
+    uint32_t* dst = kCluster > 1 ? cl.map_shared_rank(keys, 0) : keys;
     const int n = p.kb.n_blocks[i];
     const long long hs = p.kb.seg0[i] + (long long)head * p.kb.head_segs;
+    auto mean_of = [&](int b) {
+        const int seg = segment_of(p.kb, b);
+        const long long row = (hs + pages.page(p.kb, i, seg)) * p.kb.bps + (b - seg * p.kb.bps);
+        return reinterpret_cast<const float4*>(p.means + row * D) + l8;
+    };
+    float norm2 = 0.f;
     for (int b0 = (rank * kSelWarps + warp) * 4; b0 < n; b0 += kCluster * kSelWarps * 4) {
         const int b = b0 + lane / 8;
-        double s = 0, s2 = 0;
-        if (b < n) {
-            const int seg = b / p.kb.bps;
-            const long long row = (hs + pages.page(p.kb, i, seg)) * p.kb.bps + (b - seg * p.kb.bps);
-            const float4* src = reinterpret_cast<const float4*>(p.means + row * D) + l8;
-            float4 m[kRuns];
+        const float4* src = mean_of(min(b, n - 1));
+        float4 m[kRuns];
 #pragma unroll
-            for (int c = 0; c < kRuns; ++c) m[c] = __ldg(src + c * 8);
+        for (int c = 0; c < kRuns; ++c) m[c] = __ldg(src + c * 8);
+        float2 s = make_float2(0.f, 0.f), k2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < kRuns; ++c) {
-                double2 qa = make_double2(ql[c][0], ql[c][1]), qb = make_double2(ql[c][2], ql[c][3]);
-                if (PV_QS) {
-                    const volatile double2* q2 = reinterpret_cast<const volatile double2*>(qm + (c * 8 + l8) * 4);
-                    qa.x = q2[0].x; qa.y = q2[0].y; qb.x = q2[1].x; qb.y = q2[1].y;
-                }
-                s = fma(qa.x, (double)m[c].x, s);
-                s2 = fma(qa.y, (double)m[c].y, s2);
-                s = fma(qb.x, (double)m[c].z, s);
-                s2 = fma(qb.y, (double)m[c].w, s2);
-            }
-            s += s2;
+        for (int c = 0; c < kRuns; ++c) {
+            const float2 lo = make_float2(m[c].x, m[c].y), hi = make_float2(m[c].z, m[c].w);
+            s = __ffma2_rn(make_float2(ql[c].x, ql[c].y), lo, s);
+            s = __ffma2_rn(make_float2(ql[c].z, ql[c].w), hi, s);
+            k2 = __ffma2_rn(lo, lo, k2);
+            k2 = __ffma2_rn(hi, hi, k2);
         }
+        float score = s.x + s.y, len = k2.x + k2.y;
 #pragma unroll
-        for (int o = 4; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = 4; o > 0; o /= 2) {
+            score += __shfl_xor_sync(0xffffffffu, score, o);
+            len += __shfl_xor_sync(0xffffffffu, len, o);
+        }
+        // NaN lengths count as infinite: the f64 scores decide
+        norm2 = fmaxf(norm2, len == len ? len : INFINITY);
         if (l8 == 0 && b < n) {
             const bool forced = (b >= p.force0[i][0] && b < p.force1[i][0]) ||
                                 (b >= p.force0[i][1] && b < p.force1[i][1]);
-            dst[b] = forced ? ~0ull : order_key(s);
+            dst[b] = forced ? kForced | (kMaxSelectBlocks - 1 - b) : order_key(score);
         }
     }
-    if (rank == 0 && threadIdx.x == 0 && (n & 1)) keys[n] = 0;
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(norm2));
+    if (lane == 0) atomicMax(kCluster > 1 ? cl.map_shared_rank(&sh.norm2, 0) : &sh.norm2, most);
+    if (rank == 0 && threadIdx.x < 3) keys[n + threadIdx.x] = 0;   // read in fours
     if (kCluster > 1)
         cl.sync();
     else
         __syncthreads();
-    if (rank == 0)
-        write_top(keys, n, min(p.keep, n), p.keep, &sh, p.blocks + (long long)item * p.keep);
+    if (rank != 0) return;
+
+    // A score is rounded at most 2 * kRuns times along a lane's columns and
+    // four times after, each time by 2^-24 of partial sums that |qmean| |kmean|
+    // bounds; 2 * kRuns + 8 leaves room for the roundings of the lengths, the
+    // small constants for squares and products that underflow.
+    float q2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < kRuns; ++c)
+        q2 += ql[c].x * ql[c].x + ql[c].y * ql[c].y + ql[c].z * ql[c].z + ql[c].w * ql[c].w;
+#pragma unroll
+    for (int o = 4; o > 0; o /= 2) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+    float err = (2 * kRuns + 8) * 0x1p-24f * (sqrtf(q2) + 1e-18f) *
+                    (sqrtf(__uint_as_float(sh.norm2)) + 1e-18f) + 1e-36f;
+    if (!(err < INFINITY)) err = INFINITY;
+    choose(keys64, n, min(p.keep, n), p.keep, err, &sh, p.blocks + (long long)item * p.keep,
+           [&](int b) {
+               const float4* src = mean_of(b);
+               double s = 0;
+#pragma unroll
+               for (int c = 0; c < kRuns; ++c) {
+                   const float4 m = __ldg(src + c * 8);
+                   s = fma((double)ql[c].x, (double)m.x, s);
+                   s = fma((double)ql[c].y, (double)m.y, s);
+                   s = fma((double)ql[c].z, (double)m.z, s);
+                   s = fma((double)ql[c].w, (double)m.w, s);
+               }
+#pragma unroll
+               for (int o = 4; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+               return s;
+           });
 }
 
 // ------------------------------------------------------------------ copies
@@ -462,7 +563,7 @@ cudaError_t launch_select_c(const SelectParams& p, const Pages& pages, cudaStrea
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.n_items * kCluster);
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)(p.max_blocks + 1) / 2 * 16;
+    cfg.dynamicSmemBytes = std::max<size_t>(32, (size_t)p.max_blocks * 8);
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -473,22 +574,18 @@ cudaError_t launch_select_c(const SelectParams& p, const Pages& pages, cudaStrea
     return cudaLaunchKernelEx(&cfg, select_kernel<D, kCluster, Pages>, p, pages);
 }
 
-#ifndef PV_CS
-#define PV_CS 0
-#endif
 template <int D, typename Pages>
 cudaError_t launch_select_d(const SelectParams& p, const Pages& pages, cudaStream_t s) {
-    int cs = p.n_items <= 148 ? 8 : p.n_items <= 2 * 148 ? 4 : 1;
-    if (PV_CS) cs = PV_CS;
-    if (cs == 8) return launch_select_c<D, 8>(p, pages, s);
-    if (cs == 4) return launch_select_c<D, 4>(p, pages, s);
-    if (cs == 2) return launch_select_c<D, 2>(p, pages, s);
+    // few items: as many CTAs to each as still get an SM of their own, for
+    // latency (24 items of 313 blocks: 8.7 us with four, 13.5 with one); many
+    // items keep the GPU busy by themselves (1,752 items of 145 blocks: 47 us
+    // with one CTA each, 64 with two)
+    if (p.n_items * 8 <= 148) return launch_select_c<D, 8>(p, pages, s);
+    if (p.n_items * 4 <= 148) return launch_select_c<D, 4>(p, pages, s);
+    if (p.n_items * 2 <= 148) return launch_select_c<D, 2>(p, pages, s);
     return launch_select_c<D, 1>(p, pages, s);
 }
 
-#ifndef PV_SUM
-#define PV_SUM 0
-#endif
 template <int D, int kParts>
 cudaError_t launch_summary_p(const SummaryParams& p, cudaStream_t s) {
     constexpr int kPer = kPoolWarps / (D / 64 * kParts);
@@ -499,8 +596,8 @@ cudaError_t launch_summary_p(const SummaryParams& p, cudaStream_t s) {
 }
 template <int D>
 cudaError_t launch_summary_d(const SummaryParams& p, cudaStream_t s) {
-    bool few = (long long)p.n_items * p.heads * p.planes <= 4 * 148;
-    if (PV_SUM) few = PV_SUM == 4;
+    // (168 blocks of 128 x 128: 3.3 us with four warps to a strip, 6.3 with one)
+    const bool few = (long long)p.n_items * p.heads * p.planes <= 4 * 148;
     return few ? launch_summary_p<D, 4>(p, s) : launch_summary_p<D, 1>(p, s);
 }
 

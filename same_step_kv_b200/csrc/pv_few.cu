@@ -50,43 +50,56 @@ __device__ __forceinline__ uint4 few_load(const bf16* p, bool in) {
     return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
 }
 
-template <int D>
+// Transposed 8 x 8 tile of 16-bit values, a row's pair to a lane.
+__device__ __forceinline__ uint32_t few_transpose(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int D, int kRows>
 struct FewShared {
-    float o[kFewWarps][kFewRows][D];
-    float m[kFewWarps][kFewRows], l[kFewWarps][kFewRows];
+    float o[kFewWarps][kRows][D];
+    float m[kFewWarps][kRows], l[kFewWarps][kRows];
     int last;
 };
 
-template <int D, typename Pages>
-__global__ void __launch_bounds__(kFewThreads)
+// CTAs of an SM, by registers.
+constexpr int few_resident(int D, int rows) {
+    return D == 128 ? (rows == 8 ? 3 : 2) : (rows == 8 ? 4 : 3);
+}
+
+template <int D, int kRows, typename Pages>
+__global__ void __launch_bounds__(kFewThreads, few_resident(D, kRows))
     few_kernel(const __grid_constant__ FewArgs<Pages> p) {
-    __shared__ FewShared<D> sh;
+    __shared__ FewShared<D, kRows> sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int g = lane / 4, c = lane % 4;
     constexpr int kPieces = D / 32;   // 16-byte pieces of a row per lane
     constexpr int kHalves = D / 64;
+    constexpr bool kSmall = kRows == 8;
 
     int si = 0;
     while (si + 1 < p.n_streams && p.st[si + 1].cta0 <= (int)blockIdx.x) ++si;
     const FewStream& st = p.st[si];
     const int li = blockIdx.x - st.cta0;
     const int item = li / st.splits, split = li - item * st.splits;
-    const int tiles = (st.n_q + kFewRows - 1) / kFewRows;
+    const int tiles = (st.n_q + kRows - 1) / kRows;
     const int head = item / tiles, rt = item - head * tiles;
-    const int row0 = rt * kFewRows, rows = min(kFewRows, st.n_q - row0);
+    const int row0 = rt * kRows, rows = min(kRows, st.n_q - row0);
     const int groups = (st.n_q + kQBlock - 1) / kQBlock;
     const int* list = p.list ? p.list + (p.list_row0[si] + (long long)head * groups +
                                          row0 / kQBlock) * p.keep
                              : nullptr;
 
-    // Q: rows g and g + 8
-    uint4 qa[kPieces], qb[kPieces];
+    // Q: rows g and (of 16) g + 8
+    uint4 qa[kPieces], qb[kSmall ? 1 : kPieces];
     {
         const bf16* q = p.q + ((long long)st.q_row0 + (long long)head * st.n_q + row0) * D + c * 8;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             qa[i] = few_load(q + g * D + i * 32, g < rows);
-            qb[i] = few_load(q + (g + 8) * D + i * 32, g + 8 < rows);
+            if (!kSmall) qb[i] = few_load(q + (g + 8) * D + i * 32, g + 8 < rows);
         }
     }
 
@@ -112,13 +125,14 @@ __global__ void __launch_bounds__(kFewThreads)
         *row = 0;
         *valid = 0;
         if ((unsigned)b >= (unsigned)p.kb.n_blocks[si]) return;  // an empty block
-        const int seg = b / p.kb.bps, blk = b - seg * p.kb.bps;
+        const int seg = segment_of(p.kb, b), blk = b - seg * p.kb.bps;
         *valid = (blk == p.kb.bps - 1 ? p.kb.tail : kKeyTile) - k0;
         *row = (base + p.pages.page(p.kb, si, seg)) * p.kb.seg_len + blk * kKeyTile + k0;
     };
     uint4 kk[2][kPieces];       // keys g and g + 8 of the strip
     // values of keys 2c, 2c + 1, 2c + 8, 2c + 9, of this strip and the next
     uint4 vv[4][kHalves], vn[4][kHalves];
+    constexpr int kTiles = kHalves * (kSmall ? 4 : 8);   // accumulator tiles
     auto load_k = [&](long long row, int valid) {
         const bf16* k = p.k + row * D + c * 8;
 #pragma unroll
@@ -138,12 +152,13 @@ __global__ void __launch_bounds__(kFewThreads)
         }
     };
 
-    float o[kHalves * 8][4];
+    float o[kTiles][4];
 #pragma unroll
-    for (int t = 0; t < kHalves * 8; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
-    float m0 = kFewEmpty, m1 = kFewEmpty, l0 = 0.f, l1 = 0.f;   // rows g, g + 8
+    // of rows g, g + 8; of eight rows: 2c, 2c + 1
+    float m0 = kFewEmpty, m1 = kFewEmpty, l0 = 0.f, l1 = 0.f;
 
     long long row = 0;
     int valid = 0;
@@ -154,15 +169,25 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     while (u < u_end) {
         const int now = valid;
-        float s[2][4];
+        // scores: s[t] holds rows g, g + 8 at keys 8t + 2c, 8t + 2c + 1; of eight
+        // rows, s[0] holds keys g, g + 8 at rows 2c, 2c + 1
+        constexpr int kS = kSmall ? 1 : 2;
+        float s[kS][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kS; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                mma16816(s[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kk[t][i].x, kk[t][i].y);
-                mma16816(s[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kk[t][i].z, kk[t][i].w);
+        for (int i = 0; i < kPieces; ++i) {
+            if constexpr (kSmall) {
+                mma16816(s[0], kk[0][i].x, kk[1][i].x, kk[0][i].y, kk[1][i].y, qa[i].x, qa[i].y);
+                mma16816(s[0], kk[0][i].z, kk[1][i].z, kk[0][i].w, kk[1][i].w, qa[i].z, qa[i].w);
+            } else {
+#pragma unroll
+                for (int t = 0; t < kS; ++t) {
+                    mma16816(s[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kk[t][i].x, kk[t][i].y);
+                    mma16816(s[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kk[t][i].z, kk[t][i].w);
+                }
             }
         }
         if (++u < u_end) {      // the next strip, while this one is worked on
@@ -175,15 +200,24 @@ __global__ void __launch_bounds__(kFewThreads)
             load_k(row, valid);
             load_v(vn, row, valid);
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
+        float x0, x1;   // largest scores of the lane's rows
+        if constexpr (kSmall) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[t][i] = 8 * t + 2 * c + (i & 1) < now ? s[t][i] * p.scale_log2 : -INFINITY;
-        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+                s[0][i] = g + (i >> 1) * 8 < now ? s[0][i] * p.scale_log2 : -INFINITY;
+            x0 = fmaxf(s[0][0], s[0][2]);
+            x1 = fmaxf(s[0][1], s[0][3]);
+        } else {
 #pragma unroll
-        for (int d = 1; d < 4; d *= 2) {
+            for (int t = 0; t < kS; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[t][i] = 8 * t + 2 * c + (i & 1) < now ? s[t][i] * p.scale_log2 : -INFINITY;
+            x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[kS - 1][0], s[kS - 1][1]));
+            x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[kS - 1][2], s[kS - 1][3]));
+        }
+#pragma unroll
+        for (int d = kSmall ? 4 : 1; d < (kSmall ? 32 : 4); d *= 2) {
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
         }
@@ -195,21 +229,30 @@ __global__ void __launch_bounds__(kFewThreads)
             m0 = n0, m1 = n1;
             l0 *= a0, l1 *= a1;
 #pragma unroll
-            for (int t = 0; t < kHalves * 8; ++t) {
-                o[t][0] *= a0, o[t][1] *= a0;
-                o[t][2] *= a1, o[t][3] *= a1;
+            for (int t = 0; t < kTiles; ++t) {
+                o[t][0] *= a0, o[t][1] *= kSmall ? a1 : a0;
+                o[t][2] *= kSmall ? a0 : a1, o[t][3] *= a1;
             }
         }
         // P rounded to nearest bf16, its sum over the unrounded values
         uint32_t pa[4];
+        if constexpr (kSmall) {
+            const float e0 = few_ex2(s[0][0] - m0), e1 = few_ex2(s[0][1] - m1);
+            const float e2 = few_ex2(s[0][2] - m0), e3 = few_ex2(s[0][3] - m1);
+            l0 += e0 + e2;
+            l1 += e1 + e3;
+            pa[0] = few_transpose(few_pack(e0, e1));
+            pa[1] = few_transpose(few_pack(e2, e3));
+        } else {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const float e0 = few_ex2(s[t][0] - m0), e1 = few_ex2(s[t][1] - m0);
-            const float e2 = few_ex2(s[t][2] - m1), e3 = few_ex2(s[t][3] - m1);
-            l0 += e0 + e1;
-            l1 += e2 + e3;
-            pa[2 * t] = few_pack(e0, e1);
-            pa[2 * t + 1] = few_pack(e2, e3);
+            for (int t = 0; t < kS; ++t) {
+                const float e0 = few_ex2(s[t][0] - m0), e1 = few_ex2(s[t][1] - m0);
+                const float e2 = few_ex2(s[t][2] - m1), e3 = few_ex2(s[t][3] - m1);
+                l0 += e0 + e1;
+                l1 += e2 + e3;
+                pa[2 * t] = few_pack(e0, e1);
+                pa[2 * t + 1] = few_pack(e2, e3);
+            }
         }
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
@@ -218,11 +261,15 @@ __global__ void __launch_bounds__(kFewThreads)
             const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vv[2][h]);
             const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vv[3][h]);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const uint32_t sel = t & 1 ? 0x7632u : 0x5410u;
-                mma16816(o[h * 8 + t], pa[0], pa[1], pa[2], pa[3],
-                         __byte_perm(v0[t / 2], v1[t / 2], sel),
-                         __byte_perm(v2[t / 2], v3[t / 2], sel));
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t b0 = __byte_perm(v0[t], v1[t], 0x5410), b1 = __byte_perm(v2[t], v3[t], 0x5410);
+                const uint32_t b2 = __byte_perm(v0[t], v1[t], 0x7632), b3 = __byte_perm(v2[t], v3[t], 0x7632);
+                if constexpr (kSmall) {
+                    mma16816(o[h * 4 + t], b0, b2, b1, b3, pa[0], pa[1]);
+                } else {
+                    mma16816(o[h * 8 + 2 * t], pa[0], pa[1], pa[2], pa[3], b0, b1);
+                    mma16816(o[h * 8 + 2 * t + 1], pa[0], pa[1], pa[2], pa[3], b2, b3);
+                }
             }
         }
 #pragma unroll
@@ -233,25 +280,41 @@ __global__ void __launch_bounds__(kFewThreads)
 
     // the warps' results
 #pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
+    for (int d = kSmall ? 4 : 1; d < (kSmall ? 32 : 4); d *= 2) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, d);
         l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
-    if (c == 0) {
-        sh.m[warp][g] = m0, sh.m[warp][g + 8] = m1;
-        sh.l[warp][g] = l0, sh.l[warp][g + 8] = l1;
+    if (kSmall ? g == 0 : c == 0) {
+        const int r0 = kSmall ? 2 * c : g, r1 = kSmall ? 2 * c + 1 : g + 8;
+        sh.m[warp][r0] = m0, sh.m[warp][r1] = m1;
+        sh.l[warp][r0] = l0, sh.l[warp][r1] = l1;
     }
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h)
+    for (int h = 0; h < kHalves; ++h) {
+        if constexpr (kSmall) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = g + (i >> 1) * 8;
-            if (r < rows) {
-                float4* d4 = reinterpret_cast<float4*>(&sh.o[warp][r][h * 64 + c * 16 + (i & 1) * 8]);
-                d4[0] = make_float4(o[h * 8][i], o[h * 8 + 1][i], o[h * 8 + 2][i], o[h * 8 + 3][i]);
-                d4[1] = make_float4(o[h * 8 + 4][i], o[h * 8 + 5][i], o[h * 8 + 6][i], o[h * 8 + 7][i]);
+            for (int i = 0; i < 2; ++i) {
+                const int r = 2 * c + i;
+                if (r < rows) {
+                    float4* d4 = reinterpret_cast<float4*>(&sh.o[warp][r][h * 64 + g * 8]);
+                    d4[0] = make_float4(o[h * 4][i], o[h * 4][i + 2], o[h * 4 + 1][i], o[h * 4 + 1][i + 2]);
+                    d4[1] = make_float4(o[h * 4 + 2][i], o[h * 4 + 2][i + 2], o[h * 4 + 3][i],
+                                        o[h * 4 + 3][i + 2]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = g + (i >> 1) * 8;
+                if (r < rows) {
+                    float4* d4 =
+                        reinterpret_cast<float4*>(&sh.o[warp][r][h * 64 + c * 16 + (i & 1) * 8]);
+                    d4[0] = make_float4(o[h * 8][i], o[h * 8 + 1][i], o[h * 8 + 2][i], o[h * 8 + 3][i]);
+                    d4[1] = make_float4(o[h * 8 + 4][i], o[h * 8 + 5][i], o[h * 8 + 6][i], o[h * 8 + 7][i]);
+                }
             }
         }
+    }
     __syncthreads();
     const float ln2 = 0.69314718055994531f;
     const size_t slot_f = few_slot_floats(D);
@@ -289,8 +352,8 @@ __global__ void __launch_bounds__(kFewThreads)
         } else {
             __stcg(reinterpret_cast<float4*>(mine + r * D + d), acc);
             if (d == 0) {
-                __stcg(mine + kFewRows * D + r, M);
-                __stcg(mine + kFewRows * D + kFewRows + r, L);
+                __stcg(mine + kRows * D + r, M);
+                __stcg(mine + kRows * D + kRows + r, L);
             }
         }
     }
@@ -318,8 +381,8 @@ __global__ void __launch_bounds__(kFewThreads)
             for (int k = 0; k < kBatch; ++k) {
                 const bool in = k0 + k < st.splits;
                 const float* pk = parts + (size_t)(k0 + k) * slot_f;
-                mk[k] = in ? __ldcg(pk + kFewRows * D + r) : kFewEmpty;
-                lk[k] = in ? __ldcg(pk + kFewRows * D + kFewRows + r) : 0.f;
+                mk[k] = in ? __ldcg(pk + kRows * D + r) : kFewEmpty;
+                lk[k] = in ? __ldcg(pk + kRows * D + kRows + r) : 0.f;
                 ok[k] = in ? __ldcg(reinterpret_cast<const float4*>(pk + r * D + d))
                            : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -343,10 +406,17 @@ __global__ void __launch_bounds__(kFewThreads)
 
 template <typename Pages>
 cudaError_t launch_few_any(const FewArgs<Pages>& a, int head_dim, int ctas, cudaStream_t s) {
-    if (head_dim == 128)
-        few_kernel<128, Pages><<<ctas, kFewThreads, 0, s>>>(a);
-    else
-        few_kernel<64, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+    if (head_dim == 128) {
+        if (a.rows == 8)
+            few_kernel<128, 8, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+        else
+            few_kernel<128, 16, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+    } else {
+        if (a.rows == 8)
+            few_kernel<64, 8, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+        else
+            few_kernel<64, 16, Pages><<<ctas, kFewThreads, 0, s>>>(a);
+    }
     return cudaGetLastError();
 }
 
@@ -362,18 +432,20 @@ cudaError_t launch_few(const FewArgs<PageTable>& a, int head_dim, int ctas, cuda
 }
 
 bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, size_t part_floats,
-              int n_counters, int* ctas) {
+              int n_counters, int* rows, int* ctas) {
+    int most = 0;
+    for (int i = 0; i < n_streams; ++i) most = std::max(most, st[i].n_q);
+    *rows = most <= 8 ? 8 : kFewRows;
+    auto tiles = [&](int i) { return (long long)heads * ((st[i].n_q + *rows - 1) / *rows); };
     long long units = 0;
-    for (int i = 0; i < n_streams; ++i)
-        units += (long long)heads * ((st[i].n_q + kFewRows - 1) / kFewRows) * 2 * st[i].n_sel;
-    // one wave of resident CTAs (by registers: two to an SM for 128-wide
-    // heads, four for 64-wide ones), shared out by keys
-    const long long wave = (long long)n_sm * (head_dim == 128 ? 2 : 4);
+    for (int i = 0; i < n_streams; ++i) units += tiles(i) * 2 * st[i].n_sel;
+    // one wave of resident CTAs, shared out by keys
+    const long long wave = (long long)n_sm * few_resident(head_dim, *rows);
     const long long per = std::max(1LL, (units + wave - 1) / wave);
     long long cta = 0, item = 0;
     for (int i = 0; i < n_streams; ++i) {
         FewStream& s = st[i];
-        const long long items = (long long)heads * ((s.n_q + kFewRows - 1) / kFewRows);
+        const long long items = tiles(i);
         s.splits = (int)((2LL * s.n_sel + per - 1) / per);
         s.cta0 = (int)cta;
         s.item0 = (int)item;

@@ -126,6 +126,14 @@ struct KeyBlocks {
 __host__ __device__ inline bool ends_segment(const KeyBlocks& k, int b) {
     return (unsigned long long)(unsigned)(b + 1) * k.bps_inv <= k.bps_inv - 1;
 }
+// Segment of block b, likewise (quotient of b by bps).
+__host__ __device__ inline int segment_of(const KeyBlocks& k, int b) {
+#ifdef __CUDA_ARCH__
+    return k.bps == 1 ? b : (int)__umul64hi(k.bps_inv, (unsigned long long)(unsigned)b);
+#else
+    return b / k.bps;
+#endif
+}
 inline void set_blocks(KeyBlocks* k, int seg_len) {
     k->seg_len = seg_len;
     k->bps = (seg_len + kKeyTile - 1) / kKeyTile;
@@ -191,6 +199,7 @@ struct FewArgs {
     float* partial;      // few_slot_floats per CTA
     int* counters;       // arrivals per item; the last arriver resets to 0
     int heads, n_streams;
+    int rows;            // queries of an item: 8 or 16
     float scale_log2;
     const int* list;     // NULL: blocks 0 .. n_sel - 1
     int keep;
@@ -201,9 +210,9 @@ struct FewArgs {
 };
 __host__ __device__ inline size_t few_slot_floats(int D) { return (size_t)kFewRows * D + 2 * kFewRows; }
 // Lays out the streams (n_q and n_sel set; splits, cta0, item0 filled in) on
-// n_sm SMs.  False when the parts or counters do not fit.
+// n_sm SMs, in items of *rows queries.  False when the parts or counters do not fit.
 bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, size_t part_floats,
-              int n_counters, int* ctas);
+              int n_counters, int* rows, int* ctas);
 cudaError_t launch_few(const FewArgs<FixedRows>& a, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_few(const FewArgs<PageTable>& a, int head_dim, int ctas, cudaStream_t s);
 // K or V rows as segments: a box is 128 rows x 64 columns of one segment,

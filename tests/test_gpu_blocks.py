@@ -75,6 +75,35 @@ def test_select_ties_go_to_the_lowest_index(pv, nb, n_q):
         assert out[1, 0, :min(keep, nb)].tolist() == list(range(min(keep, nb)))
 
 
+@pytest.mark.parametrize("nb,close", [(40, 7), (200, 60), (900, 300), (900, 700), (3000, 600)])
+def test_select_tells_scores_apart_that_f32_cannot(pv, nb, close):
+    # `close` blocks whose scores differ in the 30th bit and later, spread over the list, the
+    # border among them: f64 decides
+    g = torch.Generator().manual_seed(nb + close)
+    m = torch.randn(1, nb, 64, generator=g) * 0.1
+    at = torch.randperm(nb, generator=g)[:close]
+    m[0, at] = torch.randn(64, generator=g)
+    m[0, at, 0] = 1.0
+    m[0, at, 1] = torch.randint(-40, 40, (close,), generator=g).float() * 2.0 ** -33
+    q = torch.randn(1, 1, 64, generator=g).to(torch.bfloat16)
+    q[0, 0, 0], q[0, 0, 1] = 4.0, 1.5
+    q, m = q.cuda(), m.cuda()
+    for keep in (1, close // 2, close - 1, min(nb, close + 3)):
+        out = torch.empty(1, 1, keep, dtype=torch.int32, device="cuda")
+        pv.pv_block_select_dense(q, m, 1, nb * 128, 1, 64, keep, 0, out)
+        assert torch.equal(out.cpu(), select64(q, m, keep)), keep
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -70, 2.0 ** -40, 2.0 ** 60, 2.0 ** 100])
+def test_select_of_very_small_and_very_large_values(pv, scale):
+    # products and squares outside f32's range
+    q = (randn(1, 2, 3, 64).float() * scale).to(torch.bfloat16)
+    m = randn(2, 2, 300, 64).float() * scale
+    out = torch.empty(2, 1, 50, dtype=torch.int32, device="cuda")
+    pv.pv_block_select_dense(q, m, 3, 300 * 128, 2, 64, 50, 1, out)
+    assert torch.equal(out.cpu(), select64(q, m, 50, [0]))
+
+
 def test_select_of_the_most_blocks(pv):
     nb = 16384
     q = randn(1, 2, 1, 64)
@@ -130,6 +159,9 @@ def reference(q, k, v, lists):
 @pytest.mark.parametrize("H,n_q,n_k,keep", [
     (1, 1, 1, 1), (2, 1, 130, 2), (3, 7, 127, 3), (1, 128, 128, 1), (2, 129, 1000, 3),
     (2, 256, 1024, 8), (3, 257, 1300, 5), (1, 300, 129, 4), (24, 1, 40007, 32), (5, 600, 5000, 17),
+    # either side of each kernel's row counts, few and many parts to an item
+    (3, 8, 3000, 9), (3, 9, 3000, 9), (1, 16, 9000, 70), (1, 17, 9000, 70), (2, 31, 300, 3),
+    (20, 32, 2000, 15), (20, 33, 2000, 15), (1, 64, 9000, 70), (1, 100, 9000, 71), (150, 3, 500, 2),
     (2, 1000, 777, 1)])
 def test_attention(pv, H, n_q, n_k, keep, D):
     q, k, v = randn(1, H, n_q, D), randn(2, H, n_k, D), randn(3, H, n_k, D)
