@@ -25,8 +25,9 @@
  *    later call.  pv_last_error() gives a one-line message for the calling
  *    thread's most recent failure.
  *  - Workspaces hold a launch's scratch state: split-KV partial results and
- *    arrival counters for attention (a handle's workspace for pv_chunk_attn,
- *    the `ws` argument for pv_attn_dense and pv_attn_varlen), the projected
+ *    arrival counters for attention (a handle's workspace for pv_chunk_attn
+ *    and pv_block_attn, the `ws` argument for pv_attn_dense, pv_attn_varlen
+ *    and pv_block_attn_dense), the projected
  *    q/k/v and their sums of squares for pv_qkv_rope_append.  Launches that
  *    use one workspace must not overlap on the GPU: issue them on one CUDA
  *    stream, or order them with events.  The host side of a handle is
@@ -162,8 +163,9 @@ PV_API pv_status pv_kv_destroy(pv_kv kv);
  *    holds them too.
  *  - pv_kv_set_state keeps the pages of frames that stay and takes free ones
  *    for the others (contents are the caller's to restore).
- *  - pv_chunk_attn reads through the page table; rows behind a frame's end
- *    are never read.
+ *  - pv_chunk_attn reads through the page table, block by block
+ *    (PV_BLOCK_KEYS); rows behind a frame's end are never read, and P is
+ *    rounded as by pv_block_attn.
  * Page ids enter a launch by value: a captured launch keeps the pages that
  * its streams held when it was captured.
  * kv_bytes: 2 * layers * steps * H * n_pages * T * D bf16.  n_pages >= F0. */
@@ -313,8 +315,9 @@ PV_API pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int 
  *  1. pv_block_summarize   mean key of each block, after the append;
  *  2. pv_block_select      the `keep` best blocks of each (head, group);
  *  3. pv_block_attn        softmax attention over the listed blocks.
- * Lists are int32 [rows][keep], one row per (stream, head, group): stream
- * i's rows start at H * (sum_{i'<i} G_i') and are [H][G_i], G = ceil(n_q / 256). */
+ * Lists are int32 [rows][keep], 1 <= keep <= 2^24, one row per (stream, head,
+ * group): stream i's rows start at H * (sum_{i'<i} G_i') and are [H][G_i],
+ * G = ceil(n_q / 256).  Forward only, like the rest of the library. */
 
 /* Bytes of the handle's block means: f32 [layers][steps][streams][H]
  * [(F0 + R) * bps][D], for a paged store [layers][steps][H][n_pages * bps][D]. */
@@ -348,8 +351,10 @@ PV_API pv_status pv_block_select(pv_kv kv, int n_streams, const int* streams, in
 /* pv_chunk_attn restricted to the first min(keep, n_blocks) entries of each
  * list row.  An index outside 0..n_blocks-1 (such as -1) stands for an empty
  * block; an index listed twice counts twice; a row without any key gives
- * out = 0 and lse = -inf.  P is rounded to nearest bf16, its sum is not
- * rounded.  Uses the handle's workspace, as pv_chunk_attn does. */
+ * out = 0 and lse = -inf.  P is rounded to nearest bf16, its sum stays f32.
+ * Results do not depend on the order in which CTAs finish.  Uses the handle's
+ * workspace, as pv_chunk_attn does.  One launch or two (a second one joins
+ * items that were split along their keys). */
 PV_API pv_status pv_block_attn(pv_kv kv, int n_streams, const int* streams, int layer, int step,
                                const void* q_rot, const int* blocks, int keep, void* out,
                                float* lse, void* cuda_stream);
@@ -360,9 +365,13 @@ PV_API pv_status pv_block_attn(pv_kv kv, int n_streams, const int* streams, int 
  *  k, v [H][n_k][D] and q [H][n_q][D] bf16, means f32 [H][nb][D],
  *  blocks int32 [H][ceil(n_q / 256)][keep], out bf16 [n_q][H][D],
  *  lse optional f32 [n_q][H].  n_front (0..keep): the first blocks, always
- *  taken.  ws: pv_block_attn_dense_ws_bytes, 256-byte aligned, zero-filled
- *  before its first use, for one launch at a time; its first int is the
- *  device error word, as for pv_attn_dense. */
+ *  taken.  Tensors, workspace and stream belong to the current device.
+ *  ws: pv_block_attn_dense_ws_bytes, 256-byte aligned, for one call at a time;
+ *  zero-filled before its first use, and again before a call with another H
+ *  or ceil(n_q / 256), which lays it out differently.  Its first int is the
+ *  device error word, as for pv_attn_dense.
+ *  No key outside the listed blocks is read: whatever lies there, or behind
+ *  the last key of a block, may be any bit pattern. */
 PV_API pv_status pv_block_summarize_dense(const void* k, int n_k, int heads, int head_dim,
                                           float* means, void* cuda_stream);
 PV_API pv_status pv_block_select_dense(const void* q, const float* means, int n_q, int n_k,

@@ -984,6 +984,13 @@ pv_status pv_qkv_rope_append(pv_kv kv, int n_streams, const int* streams, int la
 }  // extern "C"
 
 namespace {
+constexpr int kMaxKeep = 1 << 24;   // entries of a block list row
+pv_status check_keep(int keep) {
+    if (keep < 1 || keep > kMaxKeep)
+        return fail(PV_ERR_SHAPE, "keep %d outside 1..%d", keep, kMaxKeep);
+    return PV_OK;
+}
+
 // Checks shared by the calls that read a chunk's keys at (layer, step).
 pv_status check_read(pv_kv kv, int n_streams, const int* streams, int layer, int step) {
     pv_status st = check_streams(kv, n_streams, streams);
@@ -1200,7 +1207,8 @@ pv_status pv_block_attn(pv_kv kv, int n_streams, const int* streams, int layer, 
                         void* cuda_stream) {
     if (!blocks) return fail(PV_ERR_INVALID_ARG, "blocks is NULL");
     if (!aligned(blocks, 4)) return fail(PV_ERR_INVALID_ARG, "blocks must be 4-byte aligned");
-    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    const pv_status st = check_keep(keep);
+    if (st) return st;
     return store_attn(kv, n_streams, streams, layer, step, q_rot, blocks, keep, out, lse,
                       cuda_stream);
 }
@@ -1457,7 +1465,7 @@ pv_status pv_block_select(pv_kv kv, int n_streams, const int* streams, int layer
     if (!q_rot || !blocks) return fail(PV_ERR_INVALID_ARG, "NULL tensor pointer");
     if (!aligned(q_rot, 16) || !aligned(blocks, 4))
         return fail(PV_ERR_INVALID_ARG, "q_rot must be 16-byte, blocks 4-byte aligned");
-    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if ((st = check_keep(keep))) return st;
     if (force & ~(PV_FORCE_SINK | PV_FORCE_CURRENT))
         return fail(PV_ERR_INVALID_ARG, "force %d has unknown bits", force);
     if ((st = check_same_device(kv))) return st;
@@ -1573,7 +1581,7 @@ pv_status pv_block_select_dense(const void* q, const float* means, int n_q, int 
     int nb = 0;
     pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
     if (st) return st;
-    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if ((st = check_keep(keep))) return st;
     if (n_front < 0 || n_front > keep)
         return fail(PV_ERR_SHAPE, "n_front %d outside 0..keep = %d", n_front, keep);
     if (nb > kMaxSelectBlocks)
@@ -1608,7 +1616,7 @@ pv_status pv_block_attn_dense_ws_bytes(int n_q, int n_k, int heads, int head_dim
     int nb = 0;
     pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
     if (st) return st;
-    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if ((st = check_keep(keep))) return st;
     return pv_attn_dense_ws_bytes(n_q, std::min(keep, nb) * kKeyTile, heads, head_dim, ws_bytes);
 }
 
@@ -1619,7 +1627,7 @@ pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n
     int nb = 0;
     pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
     if (st) return st;
-    if (keep < 1) return fail(PV_ERR_SHAPE, "keep %d: a list holds at least one block", keep);
+    if ((st = check_keep(keep))) return st;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
         (lse && !aligned(lse, 4)) || !aligned(blocks, 4))
         return fail(PV_ERR_INVALID_ARG, "tensors must be 16-byte aligned, lse and blocks 4-byte");

@@ -139,11 +139,14 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _dense(t) -> int | None:
-    """_ptr of a tensor that has to be contiguous."""
-    if t is not None and not isinstance(t, int) and not t.is_contiguous():
-        raise PVError(PV_ERR_INVALID_ARG, "tensors must be contiguous")
-    return _ptr(t)
+def _dense(t, size: int) -> int | None:
+    """_ptr of a contiguous CUDA tensor of `size`-byte elements (or an address)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not (t.is_cuda and t.is_contiguous() and t.element_size() == size):
+        raise PVError(PV_ERR_INVALID_ARG, f"a contiguous CUDA tensor of {size}-byte elements is "
+                                          f"needed, not {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 _current = None  # (current device, raw stream of a device), once CUDA has been seen
@@ -303,26 +306,26 @@ def pv_block_summarize(kv, streams, layer, step, cuda_stream=None) -> None:
 
 def pv_block_select(kv, streams, layer, step, q_rot, keep, force, blocks, cuda_stream=None) -> None:
     n, arr = _streams(streams)
-    _check(lib.pv_block_select(kv, n, arr, layer, step, _dense(q_rot), keep, force, _dense(blocks),
+    _check(lib.pv_block_select(kv, n, arr, layer, step, _dense(q_rot, 2), keep, force, _dense(blocks, 4),
                                _stream(cuda_stream)))
 
 
 def pv_block_attn(kv, streams, layer, step, q_rot, blocks, keep, out, lse=None,
                   cuda_stream=None) -> None:
     n, arr = _streams(streams)
-    _check(lib.pv_block_attn(kv, n, arr, layer, step, _dense(q_rot), _dense(blocks), keep,
-                             _dense(out), _dense(lse), _stream(cuda_stream)))
+    _check(lib.pv_block_attn(kv, n, arr, layer, step, _dense(q_rot, 2), _dense(blocks, 4), keep,
+                             _dense(out, 2), _dense(lse, 4), _stream(cuda_stream)))
 
 
 def pv_block_summarize_dense(k, n_k, heads, head_dim, means, cuda_stream=None) -> None:
-    _check(lib.pv_block_summarize_dense(_dense(k), n_k, heads, head_dim, _dense(means),
+    _check(lib.pv_block_summarize_dense(_dense(k, 2), n_k, heads, head_dim, _dense(means, 4),
                                         _stream(cuda_stream)))
 
 
 def pv_block_select_dense(q, means, n_q, n_k, heads, head_dim, keep, n_front, blocks,
                           cuda_stream=None) -> None:
-    _check(lib.pv_block_select_dense(_dense(q), _dense(means), n_q, n_k, heads, head_dim, keep,
-                                     n_front, _dense(blocks), _stream(cuda_stream)))
+    _check(lib.pv_block_select_dense(_dense(q, 2), _dense(means, 4), n_q, n_k, heads, head_dim, keep,
+                                     n_front, _dense(blocks, 4), _stream(cuda_stream)))
 
 
 def pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep) -> int:
@@ -333,8 +336,8 @@ def pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep) -> int:
 
 def pv_block_attn_dense(q, k, v, n_q, n_k, heads, head_dim, blocks, keep, out, lse, ws, ws_bytes,
                         cuda_stream=None) -> None:
-    _check(lib.pv_block_attn_dense(_dense(q), _dense(k), _dense(v), n_q, n_k, heads, head_dim,
-                                   _dense(blocks), keep, _dense(out), _dense(lse), _dense(ws),
+    _check(lib.pv_block_attn_dense(_dense(q, 2), _dense(k, 2), _dense(v, 2), n_q, n_k, heads, head_dim,
+                                   _dense(blocks, 4), keep, _dense(out, 2), _dense(lse, 4), _dense(ws, 1),
                                    ws_bytes, _stream(cuda_stream)))
 
 

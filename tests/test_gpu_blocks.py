@@ -264,6 +264,31 @@ def test_summarize_select_attend(pv, H, D, n_q, n_k, keep, front):
     check_attention(b["out"], b["lse"], reference(q, k, v, want))
 
 
+def test_one_workspace_for_other_key_counts_and_lists(pv):
+    """Calls of one H and group count share a workspace in turn, whichever kernel they take."""
+    H, D = 3, 128
+    shapes = [(30, 5000, 20), (200, 900, 3), (5, 3000, 24), (200, 6000, 40), (30, 200, 2)] * 2
+    n = max(pv.pv_block_attn_dense_ws_bytes(a, b, H, D, c) for a, b, c in shapes)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for i, (n_q, n_k, keep) in enumerate(shapes):
+        q, k, v = randn(i, H, n_q, D), randn(40 + i, H, n_k, D), randn(80 + i, H, n_k, D)
+        lists = lists_of(i, H, n_q, blocks_of(n_k), keep)
+        out = torch.empty(n_q, H, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(n_q, H, device="cuda")
+        pv.pv_block_attn_dense(q, k, v, n_q, n_k, H, D, lists.cuda(), keep, out, lse, ws, n)
+        check_attention(out, lse, reference(q, k, v, lists), str(i))
+
+
+def test_tensors_of_another_kind_are_refused(pv):
+    q, m = randn(1, 2, 5, 64), torch.zeros(2, 3, 64, device="cuda")
+    out = torch.empty(2, 1, 2, dtype=torch.int32, device="cuda")
+    for a, b, c in ((q.float(), m, out), (q, m.bfloat16(), out), (q, m, out.long()), (q.cpu(), m, out),
+                    (q.transpose(0, 1), m, out)):
+        with pytest.raises(pv.PVError) as e:
+            pv.pv_block_select_dense(a, b, 5, 300, 2, 64, 2, 0, c)
+        assert e.value.status == pv.PV_ERR_INVALID_ARG
+
+
 def test_captured_replayed_and_on_other_streams(pv):
     H, D, n_q, n_k, keep = 3, 128, 300, 2500, 5
     sets = []

@@ -138,6 +138,7 @@ def test_forced_blocks(pv):
     W, Hh, H, D, R = 20, 15, 2, 64, 3          # 3 blocks a frame
     fixed, paged = stores(pv, W, Hh, H, D, R, pages=9)
     T, bps = W * Hh, 3
+    want = {}
     for store in (fixed, paged):
         run = Run(pv, store, 0, 1, 1)
         run.first(1)
@@ -146,7 +147,6 @@ def test_forced_blocks(pv):
         st = pv.pv_kv_get_state(store.handle, 0)
         assert (st.fill, st.slot) == (3, 1)
         sink, cur = set(range(9)), set(range(4 * bps, 5 * bps))
-        m = run.store.summary_region()
         for force, must in ((1, sink), (2, cur), (3, sink | cur)):
             keep = len(must) + 2
             blocks = torch.empty(H, 2, keep, dtype=torch.int32, device="cuda")
@@ -154,8 +154,8 @@ def test_forced_blocks(pv):
             if store is fixed:
                 k = fixed.k_region()[0, 0, 0, :, :6 * T]
                 m = means64(k.reshape(H * 6, T, D), 128).float().reshape(H, -1, D)
-                want = select64(q_rot, m, keep, sorted(must))
-            assert torch.equal(blocks.cpu(), want) if store is fixed else True
+                want[force] = select64(q_rot, m, keep, sorted(must))
+            assert torch.equal(blocks.cpu(), want[force])
             assert all(must <= set(r) for r in blocks.flatten(0, 1).tolist())
             with pytest.raises(pv.PVError) as e:
                 pv.pv_block_select(store.handle, [0], 0, 0, q_rot, len(must) - 1, force, blocks)
@@ -316,6 +316,107 @@ def test_many_streams_in_one_call(pv):
         assert (e - lse[a * T:(a + 1) * T]).abs().max() < 1e-4
         pv.pv_chunk_attn(h, [i], 0, 0, q[a], o)
         assert (o.float() - full[a * T:(a + 1) * T].float()).abs().max() < 2e-2
+    store.close()
+
+
+@pytest.mark.parametrize("D,heads", [(128, 2), (64, 5)])
+def test_projection_appends_to_pages(pv, D, heads):
+    """pv_qkv_rope_append on scattered pages writes what it writes to fixed rows."""
+    W, Hh, R, T = 12, 11, 2, 132
+    fixed, paged = stores(pv, W, Hh, heads, D, R, pages=12, layers=1)
+    pv.pv_kv_begin_chunk(paged.handle, 1, F0)       # pages 0 .. 2
+    dim = heads * D
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    w, bias = (rnd(3 * dim, dim) / dim ** 0.5).bfloat16(), rnd(3 * dim)
+    gq, gk = rnd(dim), rnd(dim)
+    for h in (fixed.handle, paged.handle):
+        pv.pv_kv_begin_chunk(h, 0, F0)
+    for chunk in range(4):
+        n = F0 * T if chunk == 0 else T
+        ws = torch.empty(pv.pv_qkv_ws_bytes(n, dim), dtype=torch.uint8, device="cuda")
+        for step in (0, 1, pv.PV_STEP_SINK) if chunk == 0 else (0, 1):
+            if step == pv.PV_STEP_SINK:
+                for h in (fixed.handle, paged.handle):
+                    pv.pv_kv_begin_sink(h, 0)
+            x = rnd(n, dim).bfloat16()
+            q = [torch.empty(heads, n, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            for h, o in zip((fixed.handle, paged.handle), q):
+                pv.pv_qkv_rope_append(h, [0], 0, step, x, w, bias, gq, gk, 1e-6, o, ws, ws.numel())
+            assert torch.equal(*q)
+        sink, ring = pv.pv_kv_page_table(paged.handle, 0)
+        pages = list(range(sink, sink + F0)) + [p for p in ring if p >= 0]
+        for a, b in ((fixed.k_region(), paged.k_region()), (fixed.v_region(), paged.v_region())):
+            for seg, page in enumerate(pages):
+                assert torch.equal(a[0, :, 0, :, seg * T:(seg + 1) * T], b[0, :, :, page * T:(page + 1) * T])
+        for h in (fixed.handle, paged.handle):
+            pv.pv_kv_begin_chunk(h, 0, 1)
+        if chunk == 1:
+            pv.pv_kv_begin_sink(paged.handle, 1)
+            pv.pv_kv_begin_chunk(paged.handle, 1, 1)    # a page between the stream's own
+    assert pv.pv_kv_poll_device_error(paged.handle) == 0
+    fixed.close(), paged.close()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_streams_in_different_phases_in_one_call(pv, paged):
+    """A first chunk (3 frames of queries) and two steady ones at different fills: one call against one each."""
+    H, D, R, W, Hh = 3, 128, 4, 17, 13
+    T = W * Hh
+    cfg = pv.make_config(1, H, D, W, Hh, ring_slots=R, steps=2, max_streams=4, max_frames=64)
+    store = pv.KVStore(cfg, pages=24 if paged else None, summaries=True)
+    h = store.handle
+    st = pv.pv_kv_state()
+    for i, (phase, chunk) in enumerate([(pv.PV_PHASE_STEADY, 2), (pv.PV_PHASE_FIRST, 0),
+                                        (pv.PV_PHASE_STEADY, 9)]):
+        st.phase, st.chunk = phase, chunk
+        pv.pv_kv_set_state(h, i, st)
+    for r in (store.k_region(), store.v_region()):
+        r.copy_(torch.randn(r.shape, device="cuda"))
+    ids, n = [2, 1, 0], [T, F0 * T, T]
+    fill = {0: 2, 1: 0, 2: 4}
+    for i in range(3):          # means of every frame: the current chunk's by the call, others plain
+        bps = blocks_of(T)
+        k, m = store.k_region(), store.summary_region()
+        if paged:
+            sink, ring = pv.pv_kv_page_table(h, i)
+            pages = list(range(sink, sink + F0)) + ring[:fill[i]]
+            for p in pages:
+                m[0, 1, :, p * bps:(p + 1) * bps] = means64(k[0, 1, :, p * T:(p + 1) * T], 128).float()
+        else:
+            for s in range(F0 + R):
+                m[0, 1, i, :, s * bps:(s + 1) * bps] = means64(k[0, 1, i, :, s * T:(s + 1) * T], 128).float()
+    before = store.summary_region().clone()
+    pv.pv_block_summarize(h, ids, 0, 1)
+    assert torch.equal(before, store.summary_region())
+    tok = sum(n)
+    q = torch.randn(H * tok, D, device="cuda").bfloat16()
+    keep = 9
+    rows = [H * -(-x // 256) for x in n]
+    blocks = torch.empty(sum(rows), keep, dtype=torch.int32, device="cuda")
+    out = torch.empty(tok, H, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(tok, H, device="cuda")
+    pv.pv_block_select(h, ids, 0, 1, q, keep, pv.PV_FORCE_CURRENT, blocks)
+    pv.pv_block_attn(h, ids, 0, 1, q, blocks, keep, out, lse)
+    t0 = r0 = 0
+    for i, x, r in zip(ids, n, rows):
+        nb = (F0 + fill[i]) * blocks_of(T)
+        one = torch.empty(r, keep, dtype=torch.int32, device="cuda")
+        qi = q[H * t0:H * (t0 + x)].view(H, x, D)
+        pv.pv_block_select(h, [i], 0, 1, qi, keep, pv.PV_FORCE_CURRENT, one)
+        assert torch.equal(one, blocks[r0:r0 + r])
+        if paged:
+            sink, ring = pv.pv_kv_page_table(h, i)
+            at = torch.cat([torch.arange(p * T, (p + 1) * T) for p in
+                            list(range(sink, sink + F0)) + ring[:fill[i]]]).cuda()
+            k, v = store.k_region()[0, 1][:, at], store.v_region()[0, 1][:, at]
+        else:
+            k, v = store.k_region()[0, 1, i], store.v_region()[0, 1, i]
+        lists = one.view(H, -1, keep).tolist()
+        check_attention(out[t0:t0 + x], lse[t0:t0 + x],
+                        attend64(qi, k, v, lambda a, g: rows_of(lists[a][g], T, nb)), f"stream {i}")
+        t0, r0 = t0 + x, r0 + r
     store.close()
 
 

@@ -343,6 +343,7 @@ def select(q=16, means=16, n_q=5, n_k=300, heads=2, head_dim=128, keep=2, n_fron
     (dict(q=None), ARG), (dict(means=None), ARG), (dict(blocks=None), ARG), (dict(q=24), ARG),
     (dict(means=8), ARG), (dict(blocks=2), ARG), (dict(n_q=0), SHAPE), (dict(n_k=0), SHAPE),
     (dict(heads=0), SHAPE), (dict(head_dim=32), SHAPE), (dict(keep=0), SHAPE),
+    (dict(keep=(1 << 24) + 1), SHAPE),
     (dict(n_front=-1), SHAPE), (dict(n_front=3), SHAPE), (dict(n_k=16384 * 128 + 1), SHAPE)])
 def test_select_dense_refusals(kw, status):
     with pytest.raises(pv.PVError) as e:
@@ -360,7 +361,7 @@ def attend(q=16, k=16, v=16, n_q=5, n_k=300, heads=2, head_dim=128, blocks=16, k
     (dict(blocks=None), ARG), (dict(q=8), ARG), (dict(k=8), ARG), (dict(v=8), ARG),
     (dict(out=8), ARG), (dict(lse=2), ARG), (dict(blocks=2), ARG), (dict(n_q=0), SHAPE),
     (dict(n_k=0), SHAPE), (dict(heads=0), SHAPE), (dict(head_dim=256), SHAPE),
-    (dict(keep=0), SHAPE), (dict(keep=-4), SHAPE), (dict(ws=None), CAP), (dict(ws=128), CAP),
+    (dict(keep=0), SHAPE), (dict(keep=-4), SHAPE), (dict(keep=1 << 30), SHAPE), (dict(ws=None), CAP), (dict(ws=128), CAP),
     (dict(ws_bytes=1000), CAP), (dict(n_q=1 << 30, heads=2), SHAPE)])
 def test_attn_dense_refusals(kw, status):
     with pytest.raises(pv.PVError) as e:
@@ -371,7 +372,7 @@ def test_attn_dense_refusals(kw, status):
 def test_attn_dense_workspace_counts_listed_blocks():
     a = pv.pv_block_attn_dense_ws_bytes(100, 5000, 2, 128, 3)
     assert a == pv.pv_attn_dense_ws_bytes(100, 3 * 128, 2, 128)
-    assert pv.pv_block_attn_dense_ws_bytes(100, 300, 2, 128, 1 << 30) == \
+    assert pv.pv_block_attn_dense_ws_bytes(100, 300, 2, 128, 1 << 24) == \
         pv.pv_attn_dense_ws_bytes(100, 3 * 128, 2, 128)
 
 
