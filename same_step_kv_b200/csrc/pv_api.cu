@@ -1052,7 +1052,6 @@ void fill_pages(const pv_kv_s* kv, int n_streams, const int* streams, PageTable*
 // What a launch over listed blocks needs besides AttnParams.
 struct BlockCall {
     const void *q, *k, *v;
-    CUtensorMap tq, tk, tv, to;
     const int* list;
     int keep;
     int list_row0[PV_MAX_STREAMS];
@@ -1063,8 +1062,10 @@ struct BlockCall {
 };
 // The kernel by query count: mma.sync with keys straight to registers for a
 // few queries, 128-row tcgen05 tiles for more.
-template <typename Pages>
-pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, cudaStream_t s) {
+// maps(&tq, &tk, &tv, &to) makes the tensor maps of the second one.
+template <typename Pages, typename Maps>
+pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, const Maps& maps,
+                        cudaStream_t s) {
     int most = 0;
     for (int i = 0; i < p.n_streams; ++i) most = std::max(most, p.st[i].n_q);
     if (most <= kFewQueries) {
@@ -1105,7 +1106,10 @@ pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, c
     std::copy(c.list_row0, c.list_row0 + p.n_streams, b.list_row0);
     b.kb = c.kb;
     b.pages = pages;
-    const cudaError_t e = launch_block_attn(c.tq, c.tk, c.tv, c.to, p, b, s);
+    CUtensorMap tq, tk, tv, to;
+    const pv_status st = maps(&tq, &tk, &tv, &to);
+    if (st) return st;
+    const cudaError_t e = launch_block_attn(tq, tk, tv, to, p, b, s);
     return e == cudaSuccess ? PV_OK : cuda_fail(e, "block attention launch");
 }
 
@@ -1163,32 +1167,33 @@ pv_status store_attn(pv_kv kv, int n_streams, const int* streams, int layer, int
         list_rows += (long long)c.heads * ((d.n_queries + kQBlock - 1) / kQBlock);
         tok += d.n_queries;
     }
-    CUtensorMap tq, to;
-    if ((st = q_map(kv, q_rot, (long long)c.heads * tok, &tq))) return st;
-    if ((st = out_map(kv, out, tok, &to))) return st;
     cudaStream_t s = (cudaStream_t)cuda_stream;
+    auto maps = [&](CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, CUtensorMap* to) -> pv_status {
+        *tk = by_block ? kv->tm_k3 : kv->tm_k;
+        *tv = by_block ? kv->tm_v3 : kv->tm_v;
+        const pv_status st = q_map(kv, q_rot, (long long)c.heads * tok, tq);
+        return st ? st : out_map(kv, out, tok, to);
+    };
     if (by_block) {
         call.q = q_rot;
         call.k = kv->kbase;
         call.v = kv->vbase;
-        call.tq = tq;
-        call.tk = kv->tm_k3;
-        call.tv = kv->tm_v3;
-        call.to = to;
         call.list = blocks;
         call.keep = keep;
         call.part_floats = (kv->wl.total - kv->wl.part_off) / sizeof(float);
         call.n_partials = kv->wl.n_partials;
         call.n_counters = kv->wl.n_counters;
         call.n_sm = kv->n_sm;
-        if (kv->n_pages == 0) return launch_blocks(p, call, FixedRows{}, s);
+        if (kv->n_pages == 0) return launch_blocks(p, call, FixedRows{}, maps, s);
         PageTable pages;
         fill_pages(kv, n_streams, streams, &pages);
-        return launch_blocks(p, call, pages, s);
+        return launch_blocks(p, call, pages, maps, s);
     }
+    CUtensorMap tq, tk, tv, to;
+    if ((st = maps(&tq, &tk, &tv, &to))) return st;
     if (plan_attention(p, kv->n_sm, kv->wl.n_partials, kv->wl.n_counters) < 0)
         return fail(PV_ERR_CAPACITY, "attention plan exceeds the workspace");
-    const cudaError_t e = launch_attn(tq, kv->tm_k, kv->tm_v, to, p, s);
+    const cudaError_t e = launch_attn(tq, tk, tv, to, p, s);
     if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
     return PV_OK;
 }
@@ -1669,13 +1674,16 @@ pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n
     call.n_partials = n_part;
     call.n_counters = n_cnt;
     call.n_sm = n_sm;
-    char msg[256];
-    if (!encode_rows_map(&call.tq, q, (long long)heads * n_q, head_dim, msg, sizeof msg) ||
-        !encode_seg_map(&call.tk, k, n_k, heads, head_dim, msg, sizeof msg) ||
-        !encode_seg_map(&call.tv, v, n_k, heads, head_dim, msg, sizeof msg) ||
-        !encode_out_map(&call.to, out, n_q, heads, head_dim, msg, sizeof msg))
-        return fail(PV_ERR_CUDA, "%s", msg);
-    return launch_blocks(p, call, FixedRows{}, (cudaStream_t)cuda_stream);
+    auto maps = [&](CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, CUtensorMap* to) -> pv_status {
+        char msg[256];
+        if (!encode_rows_map(tq, q, (long long)heads * n_q, head_dim, msg, sizeof msg) ||
+            !encode_seg_map(tk, k, n_k, heads, head_dim, msg, sizeof msg) ||
+            !encode_seg_map(tv, v, n_k, heads, head_dim, msg, sizeof msg) ||
+            !encode_out_map(to, out, n_q, heads, head_dim, msg, sizeof msg))
+            return fail(PV_ERR_CUDA, "%s", msg);
+        return PV_OK;
+    };
+    return launch_blocks(p, call, FixedRows{}, maps, (cudaStream_t)cuda_stream);
 }
 
 pv_status pv_rope_dense(pv_kv kv, int n_tokens, int frame0, const void* q, const void* k,
