@@ -42,6 +42,23 @@ def test_means_of_large_small_and_negative_values(pv):
                                                       dtype=torch.float64, device="cuda").float().double())
 
 
+@pytest.mark.parametrize("D,n", [(64, 700), (128, 700), (128, 90000)])
+def test_means_of_infinities_nan_and_subnormals(pv, D, n):
+    k = randn(n, 2, n, D)
+    inf, nan = float("inf"), float("nan")
+    for c, value in ((0, inf), (1, inf), (2, -inf), (3, nan), (4, nan), (5, 2.0 ** 127), (6, 2.0 ** 127),
+                     (7, -inf), (9, 2.0 ** -133), (10, 2.0 ** -130)):
+        k[:, 5, c] = value
+        k[1, n - 1, c] = value
+    k[0, 200, 7] = inf
+    k[0, 300:400, 9:11] = 0
+    k[0, 300, 9:11] = 2.0 ** -133
+    out = torch.empty(2, blocks_of(n), D, device="cuda")
+    pv.pv_block_summarize_dense(k, n, 2, D, out)
+    assert torch.equal(out.nan_to_num(7.0, 8.0, 9.0), means64(k, 128).float().nan_to_num(7.0, 8.0, 9.0))
+    assert out[0, 0, 1] == inf and out[0, 0, 3].isnan() and out[0, 0, 7] == -inf
+
+
 # ------------------------------------------------------------------ selection
 @pytest.mark.parametrize("H,D,n_q,n_k,keep,front", [
     (1, 64, 1, 1, 1, 0), (1, 128, 1, 1, 5, 1), (2, 128, 5, 129, 1, 0), (3, 64, 256, 2000, 4, 2),
