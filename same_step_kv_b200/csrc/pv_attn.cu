@@ -1043,9 +1043,8 @@ constexpr int kJoinCols = 16;
 constexpr int kJoinParts = 4;   // parts in flight
 template <int D>
 __global__ void __launch_bounds__(kQRows) join_kernel(const __grid_constant__ AttnParams p) {
-    // every thread waits for the end of the attention launch (this one may
-    // start before it), so that this launch cannot end first either
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the attention launch's end
+    wait_for_stream();
     constexpr int kChunks = D / kJoinCols;
     const int c0 = (int)(blockIdx.x % kChunks) * kJoinCols;
     const int X = (int)(blockIdx.x / kChunks) & 1;
@@ -1151,6 +1150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = b->tmem_base;
+    // launched early: the work before this one in the stream ends first
+    if constexpr (B::kBlocks) wait_for_stream();
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp == 0) {
@@ -1196,26 +1197,16 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
                      const CUtensorMap& to, const AttnParams& p, const B& ba, cudaStream_t s) {
     using C = Cfg<D>;
     static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(attn_kernel<D, kRun, B>, C::kSmem, configured);
+    cudaError_t e = smem_limit_once(attn_kernel<D, kRun, B>, C::kSmem, configured);
     if (e != cudaSuccess) return e;
-    attn_kernel<D, kRun, B><<<p.grid, kThreads, C::kSmem, s>>>(tq, tk, tv, to, p, ba);
-    if (B::kBlocks && !kRun && any_split(p)) {
-        const cudaError_t e2 = cudaGetLastError();
-        if (e2 != cudaSuccess) return e2;
-        // programmatic: its launch overlaps the last CTAs of the first one
-        // (chunk of 880 queries over 37 blocks: 69.7 -> 68.8 us)
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)p.n_items * 2 * (D / kJoinCols));
-        cfg.blockDim = dim3(kQRows);
-        cfg.stream = s;
-        cudaLaunchAttribute at{};
-        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+    if constexpr (!B::kBlocks) {
+        attn_kernel<D, kRun, B><<<p.grid, kThreads, C::kSmem, s>>>(tq, tk, tv, to, p, ba);
+        return cudaGetLastError();
+    } else {
+        e = launch_early(attn_kernel<D, kRun, B>, p.grid, kThreads, C::kSmem, 1, s, tq, tk, tv, to, p, ba);
+        if (e != cudaSuccess || kRun || !any_split(p)) return e;
+        return launch_early(join_kernel<D>, p.n_items * 2 * (D / kJoinCols), kQRows, 0, 1, s, p);
     }
-    return cudaGetLastError();
 }
 
 template <typename B>

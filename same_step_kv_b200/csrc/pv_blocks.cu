@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kPoolThreads, 3)
     constexpr int kStrips = D / 64;
     constexpr int kPer = kPoolWarps / (kStrips * kParts);    // blocks of a CTA
     __shared__ double part[kParts > 1 ? kPoolWarps * 64 : 1];
+    wait_for_stream();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int strip = warp / kParts % kStrips, share = warp % kParts;
     const long long idx = (long long)blockIdx.x * kPer + warp / (kStrips * kParts);
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kSelThreads, 4)
     __shared__ SelShared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int item = blockIdx.x / kCluster;
+    wait_for_stream();
     if (threadIdx.x == 0) {
         sh.norm2 = 0;
         sh.edge = 0xFFFFFFFFu;
@@ -560,18 +562,10 @@ cudaError_t launch_select_c(const SelectParams& p, const Pages& pages, cudaStrea
     cudaError_t e =
         smem_limit_once(select_kernel<D, kCluster, Pages>, kMaxSelectBlocks * 8, configured);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.n_items * kCluster);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = std::max<size_t>(32, (size_t)p.max_blocks * 8);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = kCluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D, kCluster, Pages>, p, pages);
+    // (the list of a short sequence still has room for reads in fours)
+    const size_t smem = std::max<size_t>(32, (size_t)p.max_blocks * 8);
+    return launch_early(select_kernel<D, kCluster, Pages>, (unsigned)p.n_items * kCluster,
+                        kSelThreads, smem, kCluster, s, p, pages);
 }
 
 template <int D, typename Pages>
@@ -591,8 +585,8 @@ cudaError_t launch_summary_p(const SummaryParams& p, cudaStream_t s) {
     constexpr int kPer = kPoolWarps / (D / 64 * kParts);
     const long long ctas = ((long long)p.n_items * p.heads + kPer - 1) / kPer;
     if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-    summary_kernel<D, kParts><<<dim3((unsigned)ctas, p.planes), kPoolThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(summary_kernel<D, kParts>, dim3((unsigned)ctas, p.planes), kPoolThreads, 0,
+                        1, s, p);
 }
 template <int D>
 cudaError_t launch_summary_d(const SummaryParams& p, cudaStream_t s) {

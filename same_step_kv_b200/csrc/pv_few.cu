@@ -2,24 +2,33 @@
 // short query sets, where the 128-row tiles of the tcgen05 kernel would be
 // almost empty and reading K and V is all the time there is.
 //
-// An item is (stream, head, 16 queries).  Its keys, in units of 64, are cut
-// into even parts, one CTA of four warps to a part, so that few items fill the
-// GPU; a warp takes 16 keys of each unit.  Keys and values go from
-// global memory straight into the operand registers of mma.sync.m16n8k16
-// (M = the 16 queries): nothing is staged, so nothing waits at a barrier
-// inside the key loop, and a warp has its next keys in flight while it
-// works.  Running maximum and sum per warp as in the other kernels; the four
-// warps join through shared memory, the parts of an item through global
-// memory by the last CTA to arrive, in part order.
+// An item is (stream, head, 16 queries), or 8 when no stream has more.  Its
+// keys, in units of 64, are cut into even parts, one CTA of four warps to a
+// part, so that few items fill the GPU; a warp takes 16 keys of each unit.
+// Keys and values go from global memory straight into the operand registers
+// of mma.sync.m16n8k16: nothing is staged, so nothing waits at a barrier
+// inside the key loop, and a warp has its next keys in flight while it works.
+// Running maximum and sum per warp as in the other kernels; the four warps
+// join through shared memory, the parts of an item through global memory by
+// the last CTA to arrive, in part order.
 //
 // Operand registers.  With g = lane / 4 and c = lane % 4, mma wants from a
 // lane A rows g, g + 8 and B column g, each at k = 2c, 2c + 1, 2c + 8, 2c + 9.
-//  S = Q K^T: the order of the k positions is free as long as Q and K agree,
-//   so lane c takes the 16-byte pieces c, c + 4, c + 8, ... of a row, eight
+//  16 queries: S = Q K^T and O = P V, queries along M.
+//  8 queries: S^T = K Q^T and O^T = V^T P^T, keys and columns along M: half
+//   the products and accumulators; P^T turns into an operand by a transpose
+//   of its 8 x 8 tiles.
+//  The order of the k positions of S is free as long as Q and K agree, so
+//   lane c takes the 16-byte pieces c, c + 4, c + 8, ... of a row, eight
 //   dimensions that serve two k steps.
-//  O = P V: the order of the columns is free, so column g of tile t stands
-//   for column 8 g + t of a 64-column half, and a lane's eight tiles come
-//   from one 16-byte piece of each of its four key rows.
+//  The order of the columns of O is free, so column g of tile t stands for
+//   column 8 g + t of a 64-column half, and a lane's tiles come from one
+//   16-byte piece of each of its four key rows.
+//
+// Measured, 24 heads of 128, one query over 32 of 313 blocks (50.3 MB): 15 us,
+// 3.4 TB/s; the tcgen05 kernel 28 us.  The call's fixed chain (launch, list,
+// first keys, joins) is about 6 us of it.  Drawing later strips into L2 ahead
+// of time (cp.async.bulk.prefetch) made it slower, 18 against 16.6 us.
 #include "pv_internal.h"
 
 namespace pv {
@@ -73,6 +82,7 @@ template <int D, int kRows, typename Pages>
 __global__ void __launch_bounds__(kFewThreads, few_resident(D, kRows))
     few_kernel(const __grid_constant__ FewArgs<Pages> p) {
     __shared__ FewShared<D, kRows> sh;
+    wait_for_stream();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int g = lane / 4, c = lane % 4;
     constexpr int kPieces = D / 32;   // 16-byte pieces of a row per lane
@@ -406,18 +416,11 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(D, kRows))
 
 template <typename Pages>
 cudaError_t launch_few_any(const FewArgs<Pages>& a, int head_dim, int ctas, cudaStream_t s) {
-    if (head_dim == 128) {
-        if (a.rows == 8)
-            few_kernel<128, 8, Pages><<<ctas, kFewThreads, 0, s>>>(a);
-        else
-            few_kernel<128, 16, Pages><<<ctas, kFewThreads, 0, s>>>(a);
-    } else {
-        if (a.rows == 8)
-            few_kernel<64, 8, Pages><<<ctas, kFewThreads, 0, s>>>(a);
-        else
-            few_kernel<64, 16, Pages><<<ctas, kFewThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    if (head_dim == 128)
+        return a.rows == 8 ? launch_early(few_kernel<128, 8, Pages>, ctas, kFewThreads, 0, 1, s, a)
+                           : launch_early(few_kernel<128, 16, Pages>, ctas, kFewThreads, 0, 1, s, a);
+    return a.rows == 8 ? launch_early(few_kernel<64, 8, Pages>, ctas, kFewThreads, 0, 1, s, a)
+                       : launch_early(few_kernel<64, 16, Pages>, ctas, kFewThreads, 0, 1, s, a);
 }
 
 static_assert(sizeof(FewArgs<PageTable>) <= 32000, "kernel parameters too large");

@@ -24,6 +24,37 @@ constexpr int kQBlock = kQRows * kQTilesPerCta;
 constexpr int kKeyTile = 128;             // keys per K/V tile (MMA N of Q K^T)
 constexpr int kMaxGrid = 160;             // CTAs of one attention launch at most (>= SMs)
 
+// ---------------------------------------------------------------- early launches
+// A launch that may start while the one before it in the stream still runs,
+// so that its launch and set-up overlap that one's end.  Its kernel calls
+// wait_for_stream in every thread before it touches global memory: nothing of
+// it is seen to happen early, and it cannot end before the launch it follows.
+// Chunk of 880 queries over 37 blocks, two launches a call: 72.9 -> 70.5 us;
+// four streams of 64-wide heads: 91.3 -> 88.7 us.
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename K, typename... A>
+cudaError_t launch_early(K kernel, dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                         cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // ---------------------------------------------------------------- RoPE + append
 struct RopeStreamDesc {
     int in_tok0;                     // first token of this stream in the packed input
