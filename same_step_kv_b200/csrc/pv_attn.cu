@@ -1036,7 +1036,7 @@ __device__ void softmax_epilogue(const AttnParams& p, const B& ba, const CUtenso
 
 // Merge of the split items of a launch over listed blocks, as a launch of its
 // own: with few items an item has many parts, and one CTA reading them all
-// took most of the time (4 heads, 128 queries, 32 blocks: 95 us, against 18
+// took most of the time (4 heads, 128 queries, 32 blocks: 95 us, against 14
 // with this).  One CTA per (item, query tile, 16 columns), a thread per row,
 // parts in order; bound by latency.
 constexpr int kJoinCols = 16;

@@ -571,9 +571,9 @@ cudaError_t launch_select_c(const SelectParams& p, const Pages& pages, cudaStrea
 template <int D, typename Pages>
 cudaError_t launch_select_d(const SelectParams& p, const Pages& pages, cudaStream_t s) {
     // few items: as many CTAs to each as still get an SM of their own, for
-    // latency (24 items of 313 blocks: 8.7 us with four, 13.5 with one); many
-    // items keep the GPU busy by themselves (1,752 items of 145 blocks: 47 us
-    // with one CTA each, 64 with two)
+    // latency (24 items of 313 blocks: 8.0 us with four, 11.1 with one); many
+    // items keep the GPU busy by themselves (1,752 items of 145 blocks: 38.7 us
+    // with one CTA each, 56 with two)
     if (p.n_items * 8 <= 148) return launch_select_c<D, 8>(p, pages, s);
     if (p.n_items * 4 <= 148) return launch_select_c<D, 4>(p, pages, s);
     if (p.n_items * 2 <= 148) return launch_select_c<D, 2>(p, pages, s);
@@ -590,7 +590,8 @@ cudaError_t launch_summary_p(const SummaryParams& p, cudaStream_t s) {
 }
 template <int D>
 cudaError_t launch_summary_d(const SummaryParams& p, cudaStream_t s) {
-    // (168 blocks of 128 x 128: 3.3 us with four warps to a strip, 6.3 with one)
+    // 168 blocks of 128 x 128: 3.1 us with four warps to a strip, 5.1 with one;
+    // 3,480 blocks: 24.6 and 22.5 us
     const bool few = (long long)p.n_items * p.heads * p.planes <= 4 * 148;
     return few ? launch_summary_p<D, 4>(p, s) : launch_summary_p<D, 1>(p, s);
 }

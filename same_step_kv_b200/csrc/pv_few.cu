@@ -25,9 +25,9 @@
 //   column 8 g + t of a 64-column half, and a lane's tiles come from one
 //   16-byte piece of each of its four key rows.
 //
-// Measured, 24 heads of 128, one query over 32 of 313 blocks (50.3 MB): 15 us,
-// 3.4 TB/s; the tcgen05 kernel 28 us.  The call's fixed chain (launch, list,
-// first keys, joins) is about 6 us of it.  Drawing later strips into L2 ahead
+// Measured, 24 heads of 128, one query over 32 of 313 blocks (50.3 MB): 14 us;
+// the tcgen05 kernel 20 us.  The call's fixed chain (launch, list, first keys,
+// joins) is about 6 us of it.  Drawing later strips into L2 ahead
 // of time (cp.async.bulk.prefetch) made it slower, 18 against 16.6 us.
 #include "pv_internal.h"
 
@@ -440,8 +440,22 @@ bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, s
     for (int i = 0; i < n_streams; ++i) most = std::max(most, st[i].n_q);
     *rows = most <= 8 ? 8 : kFewRows;
     auto tiles = [&](int i) { return (long long)heads * ((st[i].n_q + *rows - 1) / *rows); };
-    long long units = 0;
-    for (int i = 0; i < n_streams; ++i) units += tiles(i) * 2 * st[i].n_sel;
+    long long units = 0, blocks = 0, groups = 0;
+    for (int i = 0; i < n_streams; ++i) {
+        units += tiles(i) * 2 * st[i].n_sel;
+        blocks += (long long)heads * st[i].n_sel;
+        groups += heads;
+    }
+    // Microseconds of this kernel and of the tcgen05 one (whose split items
+    // cost a join that grows with their parts).  24 heads of 128, one query:
+    // 8 blocks 6.7 against 12.7, 32 blocks 13.8 against 20.1, 128 blocks 50.2
+    // against 45.2; 24 queries, 8 blocks 11.7 against 12.9, 32 blocks 22.8
+    // against 20.3; one head, 24 queries over 300 blocks 25.4 against 34.6.
+    const double unit = head_dim == 128 ? (*rows == 8 ? 0.0079 : 0.0097) : (*rows == 8 ? 0.0045 : 0.0055);
+    const double tile = head_dim == 128 ? 0.0109 : 0.0095;
+    const double few = 4.0 + unit * units;
+    const double many = 10.5 + tile * blocks + 0.16 * std::min<double>(n_sm, (double)blocks) / groups;
+    if (few > many) return false;
     // one wave of resident CTAs, shared out by keys
     const long long wave = (long long)n_sm * few_resident(head_dim, *rows);
     const long long per = std::max(1LL, (units + wave - 1) / wave);
@@ -449,7 +463,11 @@ bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, s
     for (int i = 0; i < n_streams; ++i) {
         FewStream& s = st[i];
         const long long items = tiles(i);
-        s.splits = (int)((2LL * s.n_sel + per - 1) / per);
+        // one CTA joins an item's parts: the more rows, the fewer parts (one head,
+        // 128 blocks: one query 10 us with 60 parts, 16 with 256; 16 queries 16
+        // with 32, 46 with 256)
+        s.splits = (int)std::min((2LL * s.n_sel + per - 1) / per,
+                                 1024LL / (kFewRows + std::min(*rows, s.n_q)));
         s.cta0 = (int)cta;
         s.item0 = (int)item;
         cta += items * s.splits;

@@ -241,7 +241,8 @@ struct FewArgs {
 };
 __host__ __device__ inline size_t few_slot_floats(int D) { return (size_t)kFewRows * D + 2 * kFewRows; }
 // Lays out the streams (n_q and n_sel set; splits, cta0, item0 filled in) on
-// n_sm SMs, in items of *rows queries.  False when the parts or counters do not fit.
+// n_sm SMs, in items of *rows queries.  False when the parts or counters do
+// not fit, or the tcgen05 kernel is expected to take less time.
 bool plan_few(FewStream* st, int n_streams, int heads, int head_dim, int n_sm, size_t part_floats,
               int n_counters, int* rows, int* ctas);
 cudaError_t launch_few(const FewArgs<FixedRows>& a, int head_dim, int ctas, cudaStream_t s);
