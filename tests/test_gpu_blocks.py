@@ -339,3 +339,49 @@ def test_captured_replayed_and_on_other_streams(pv):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(b[x], y) for x, y in zip(("blocks", "out", "lse"), w))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_from_copies_memsets_and_other_streams(pv, captured):
+    """The calls wait for whatever came before them in the stream: a copy, a memset, a kernel, work of
+    another stream; and what comes after waits for them."""
+    H, D, n_q, n_k, keep = 3, 128, 300, 2500, 5
+    q, k, v = randn(1, H, n_q, D), randn(2, H, n_k, D), randn(3, H, n_k, D)
+    b = buffers(pv, H, n_q, n_k, D, keep)
+    big = torch.randn(40_000_000, device="cuda")
+    pipeline(pv, q, k, v, keep, 1, b)
+    want = [b[x].clone() for x in ("means", "blocks", "out", "lse")]
+    qc, kc, vc = (torch.empty_like(t) for t in (q, k, v))
+    side = torch.cuda.Stream()
+    got = [torch.empty_like(w) for w in want]
+
+    def body():
+        here = torch.cuda.current_stream()
+        for t in (qc, kc, vc, *(b[x] for x in ("means", "blocks", "out", "lse"))):
+            t.zero_()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            big.mul_(1.0)
+            kc.copy_(k)
+        big.add_(0.0)
+        qc.copy_(q)
+        vc.copy_(v)
+        here.wait_stream(side)
+        pipeline(pv, qc, kc, vc, keep, 1, b)
+        for g, x in zip(got, ("means", "blocks", "out", "lse")):
+            g.copy_(b[x])
+            b[x].zero_()
+
+    if captured:
+        body()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            body()
+        for _ in range(5):
+            graph.replay()
+    else:
+        for _ in range(5):
+            body()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
