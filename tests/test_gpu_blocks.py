@@ -385,3 +385,25 @@ def test_inputs_from_copies_memsets_and_other_streams(pv, captured):
             body()
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("n_q", [20, 300])
+def test_offsets_beyond_32_bits(pv, n_q):
+    """12 heads of 2,000,077 keys: 3.1e9 values of K and of V; the last head is checked."""
+    H, n_k, D, keep, h = 12, 2_000_077, 128, 6, 11
+    nb = blocks_of(n_k)
+    k, v = (torch.empty(H, n_k, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for i in range(H):
+        k[i], v[i] = randn(i, n_k, D), randn(100 + i, n_k, D)
+    q = randn(7, H, n_q, D)
+    b = buffers(pv, H, n_q, n_k, D, keep)
+    pipeline(pv, q, k, v, keep, 1, b)
+    m = means64(k[h:], 128).float()
+    assert torch.equal(b["means"][h:], m)
+    assert torch.equal(b["blocks"][h:].cpu(), select64(q[h:], m, keep, [0]))
+    lists = b["blocks"]
+    lists[:, :, -1] = nb - 1       # the ragged last block
+    pv.pv_block_attn_dense(q, k, v, n_q, n_k, H, D, lists, keep, b["out"], b["lse"], b["ws"], b["n"])
+    t = lists[h:].tolist()
+    check_attention(b["out"][:, h:], b["lse"][:, h:],
+                    attend64(q[h:], k[h:], v[h:], lambda a, g: rows_of(t[a][g], n_k, nb)))

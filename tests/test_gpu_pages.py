@@ -359,6 +359,43 @@ def test_projection_appends_to_pages(pv, D, heads):
     fixed.close(), paged.close()
 
 
+def test_a_store_beyond_32_bit_offsets(pv):
+    """100 pages of 880 x 24 x 128 in 16 planes: 4.3e9 values of K and of V; the last plane is used."""
+    H, D, R, L, S, T, n = 24, 128, 18, 4, 4, 880, 100
+    cfg = pv.make_config(L, H, D, 40, 22, ring_slots=R, steps=S, max_streams=4)
+    store = pv.KVStore(cfg, pages=n, summaries=True)
+    h = store.handle
+    st = pv.pv_kv_state()
+    st.phase, st.chunk = pv.PV_PHASE_STEADY, 18
+    for i in range(4):
+        pv.pv_kv_set_state(h, i, st)          # 21 pages each: stream 3 in 63 .. 83
+    K, V = store.k_region()[3, 3], store.v_region()[3, 3]
+    K.copy_(torch.randn(K.shape, device="cuda")), V.copy_(torch.randn(V.shape, device="cuda"))
+    k, v = K[:, 63 * T:84 * T].clone(), V[:, 63 * T:84 * T].clone()
+    q = torch.randn(H, T, D, device="cuda").bfloat16()
+    out, lse = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, device="cuda")
+    lists = torch.randint(0, 147, (H, 4, 5), dtype=torch.int32, device="cuda")
+    t = lists.tolist()
+    ref = attend64(q, k, v, lambda a, g: rows_of(t[a][g], T, 147))
+    pv.pv_block_attn(h, [3], 3, 3, q, lists, 5, out, lse)
+    check_attention(out, lse, ref)
+    pv.pv_block_summarize(h, [3], 3, 3)
+    assert torch.equal(store.summary_region()[3, 3][:, 83 * 7:84 * 7],
+                       means64(k[:, 20 * T:], 128).float())
+    # the page in hand copied beyond the others, then everything moved down
+    pv.pv_kv_release(h, 0)
+    pv.pv_kv_fork(h, 3, [0], 1)               # page 0
+    assert torch.equal(K[:, :T], k[:, 20 * T:])
+    assert pv.pv_kv_compact(h) == 63
+    assert pv.pv_kv_page_table(h, 3)[0] == 43
+    assert torch.equal(K[:, 43 * T:64 * T], k) and torch.equal(V[:, 43 * T:64 * T], v)
+    for i in (3, 0):
+        out.zero_()
+        pv.pv_block_attn(h, [i], 3, 3, q, lists, 5, out, lse)
+        check_attention(out, lse, ref)
+    store.close()
+
+
 @pytest.mark.parametrize("paged", [False, True])
 def test_streams_in_different_phases_in_one_call(pv, paged):
     """A first chunk (3 frames of queries) and two steady ones at different fills: one call against one each."""
