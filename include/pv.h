@@ -366,10 +366,10 @@ PV_API pv_status pv_block_attn(pv_kv kv, int n_streams, const int* streams, int 
  *  blocks int32 [H][ceil(n_q / 256)][keep], out bf16 [n_q][H][D],
  *  lse optional f32 [n_q][H].  n_front (0..keep): the first blocks, always
  *  taken.  Tensors, workspace and stream belong to the current device.
- *  ws: pv_block_attn_dense_ws_bytes, 256-byte aligned, for one call at a time;
- *  zero-filled before its first use, and again before a call with another H
- *  or ceil(n_q / 256), which lays it out differently.  Its first int is the
- *  device error word, as for pv_attn_dense.
+ *  ws: pv_block_attn_dense_ws_bytes, 256-byte aligned, zero-filled before its
+ *  first use, for one call at a time; one workspace serves calls of any
+ *  shape that it is large enough for.  Its first int is the device error
+ *  word, as for pv_attn_dense.
  *  No key outside the listed blocks is read: whatever lies there, or behind
  *  the last key of a block, may be any bit pattern. */
 PV_API pv_status pv_block_summarize_dense(const void* k, int n_k, int heads, int head_dim,

@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1056,8 +1057,11 @@ struct BlockCall {
     int keep;
     int list_row0[PV_MAX_STREAMS];
     KeyBlocks kb;
-    size_t part_floats;     // workspace: partial results and arrival counters
-    int n_partials, n_counters;
+    size_t part_floats;     // workspace: partial results
+    int n_partials;
+    int* few_counters;      // arrival counters of the few-query kernel
+    int n_few;
+    int n_counters;         // items that the tcgen05 kernel's plan may have, times two
     int n_sm;
 };
 // The kernel by query count: mma.sync with keys straight to registers for a
@@ -1077,7 +1081,7 @@ pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, c
             f.st[i].n_sel = p.st[i].n_k / kKeyTile;
         }
         int ctas = 0;
-        if (plan_few(f.st, p.n_streams, p.heads, p.head_dim, c.n_sm, c.part_floats, c.n_counters,
+        if (plan_few(f.st, p.n_streams, p.heads, p.head_dim, c.n_sm, c.part_floats, c.n_few,
                      &f.rows, &ctas)) {
             f.q = (const bf16*)c.q;
             f.k = (const bf16*)c.k;
@@ -1085,7 +1089,7 @@ pv_status launch_blocks(AttnParams& p, const BlockCall& c, const Pages& pages, c
             f.out = p.out;
             f.lse = p.lse;
             f.partial = p.partial;
-            f.counters = p.counters;
+            f.counters = c.few_counters;
             f.heads = p.heads;
             f.n_streams = p.n_streams;
             f.scale_log2 = p.scale_log2;
@@ -1182,7 +1186,8 @@ pv_status store_attn(pv_kv kv, int n_streams, const int* streams, int layer, int
         call.keep = keep;
         call.part_floats = (kv->wl.total - kv->wl.part_off) / sizeof(float);
         call.n_partials = kv->wl.n_partials;
-        call.n_counters = kv->wl.n_counters;
+        call.few_counters = p.counters;
+        call.n_few = call.n_counters = kv->wl.n_counters;
         call.n_sm = kv->n_sm;
         if (kv->n_pages == 0) return launch_blocks(p, call, FixedRows{}, maps, s);
         PageTable pages;
@@ -1542,6 +1547,16 @@ pv_status dense_blocks(int n_q, int n_k, int heads, int head_dim, int* nb) {
     *nb = (n_k + kKeyTile - 1) / kKeyTile;
     return PV_OK;
 }
+// Workspace of pv_block_attn_dense: error word, the hand-out's two counters,
+// the few-query kernel's arrival counters, partial results.  What has to be
+// zero before a call lies at the same place for every shape.
+constexpr size_t kBlockHandOut = 64, kBlockFew = 256;
+constexpr int kBlockFewCounters = 16384;
+constexpr size_t kBlockParts = kBlockFew + kBlockFewCounters * sizeof(int);
+size_t block_partials(int heads, int n_q, int n_sel) {
+    const size_t n_qb = (n_q + kQBlock - 1) / kQBlock;
+    return 4 * std::min<size_t>(kMaxGrid, (size_t)heads * n_qb * n_sel);
+}
 KeyBlocks one_segment(int n_k, int nb) {
     KeyBlocks kb{};
     set_blocks(&kb, n_k);
@@ -1622,7 +1637,9 @@ pv_status pv_block_attn_dense_ws_bytes(int n_q, int n_k, int heads, int head_dim
     pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
     if (st) return st;
     if ((st = check_keep(keep))) return st;
-    return pv_attn_dense_ws_bytes(n_q, std::min(keep, nb) * kKeyTile, heads, head_dim, ws_bytes);
+    *ws_bytes = kBlockParts + block_partials(heads, n_q, std::min(keep, nb)) *
+                                  partial_slot_floats(head_dim) * sizeof(float);
+    return PV_OK;
 }
 
 pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n_q, int n_k,
@@ -1645,18 +1662,13 @@ pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n
     if ((st = check_async("an earlier launch"))) return st;
     int n_sm = 148;
     if ((st = check_device(&n_sm))) return st;
-    const size_t n_qb = (n_q + kQBlock - 1) / kQBlock;
-    const size_t cnt = (size_t)heads * n_qb * kQTilesPerCta;
-    if (cnt >= (1ull << 31)) return fail(PV_ERR_SHAPE, "too many query groups");
-    const int n_cnt = (int)cnt;
-    const size_t tiles = (size_t)heads * n_qb * n_sel;
-    const int n_part = (int)(4 * std::min<size_t>(kMaxGrid, tiles));
+    const int n_part = (int)block_partials(heads, n_q, n_sel);
     AttnParams p{};
     p.out = (bf16*)out;
     p.lse = lse;
     p.err = (int*)ws;
-    p.counters = (int*)((char*)ws + 256);
-    p.partial = (float*)((char*)ws + 256 + round_up((size_t)n_cnt * sizeof(int), 256));
+    p.counters = (int*)((char*)ws + kBlockHandOut);
+    p.partial = (float*)((char*)ws + kBlockParts);
     p.heads = heads;
     p.head_dim = head_dim;
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
@@ -1672,7 +1684,9 @@ pv_status pv_block_attn_dense(const void* q, const void* k, const void* v, int n
     call.kb = one_segment(n_k, nb);
     call.part_floats = n_part * partial_slot_floats(head_dim);
     call.n_partials = n_part;
-    call.n_counters = n_cnt;
+    call.few_counters = (int*)((char*)ws + kBlockFew);
+    call.n_few = kBlockFewCounters;
+    call.n_counters = INT_MAX;
     call.n_sm = n_sm;
     auto maps = [&](CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, CUtensorMap* to) -> pv_status {
         char msg[256];

@@ -281,19 +281,22 @@ def test_summarize_select_attend(pv, H, D, n_q, n_k, keep, front):
     check_attention(b["out"], b["lse"], reference(q, k, v, want))
 
 
-def test_one_workspace_for_other_key_counts_and_lists(pv):
-    """Calls of one H and group count share a workspace in turn, whichever kernel they take."""
-    H, D = 3, 128
-    shapes = [(30, 5000, 20), (200, 900, 3), (5, 3000, 24), (200, 6000, 40), (30, 200, 2)] * 2
-    n = max(pv.pv_block_attn_dense_ws_bytes(a, b, H, D, c) for a, b, c in shapes)
+def test_one_workspace_for_calls_of_any_shape(pv):
+    """Heads, queries, keys, lists and head dimensions change from call to call, and with them the
+    kernel and the way the work is shared out."""
+    shapes = [(3, 128, 30, 5000, 20), (3, 128, 200, 900, 3), (40, 64, 700, 3000, 24), (3, 128, 5, 3000, 24),
+              (2, 64, 1100, 6000, 40), (24, 128, 1, 9000, 60), (50, 64, 2000, 200, 2), (3, 128, 30, 200, 2),
+              (24, 64, 20, 4000, 7)] * 2
+    n = max(pv.pv_block_attn_dense_ws_bytes(a, b, h, d, c) for h, d, a, b, c in shapes)
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
-    for i, (n_q, n_k, keep) in enumerate(shapes):
+    for i, (H, D, n_q, n_k, keep) in enumerate(shapes):
         q, k, v = randn(i, H, n_q, D), randn(40 + i, H, n_k, D), randn(80 + i, H, n_k, D)
         lists = lists_of(i, H, n_q, blocks_of(n_k), keep)
-        out = torch.empty(n_q, H, D, dtype=torch.bfloat16, device="cuda")
-        lse = torch.empty(n_q, H, device="cuda")
+        out = torch.zeros(n_q, H, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(n_q, H, device="cuda")
         pv.pv_block_attn_dense(q, k, v, n_q, n_k, H, D, lists.cuda(), keep, out, lse, ws, n)
         check_attention(out, lse, reference(q, k, v, lists), str(i))
+    assert pv.pv_attn_poll_device_error(ws, n) == 0
 
 
 def test_tensors_of_another_kind_are_refused(pv):

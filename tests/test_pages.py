@@ -370,10 +370,11 @@ def test_attn_dense_refusals(kw, status):
 
 
 def test_attn_dense_workspace_counts_listed_blocks():
-    a = pv.pv_block_attn_dense_ws_bytes(100, 5000, 2, 128, 3)
-    assert a == pv.pv_attn_dense_ws_bytes(100, 3 * 128, 2, 128)
-    assert pv.pv_block_attn_dense_ws_bytes(100, 300, 2, 128, 1 << 24) == \
-        pv.pv_attn_dense_ws_bytes(100, 3 * 128, 2, 128)
+    size = lambda *a: pv.pv_block_attn_dense_ws_bytes(*a)  # noqa: E731
+    slot = (128 * 128 + 2 * 128) * 4
+    assert size(100, 5000, 2, 128, 3) - size(100, 5000, 1, 128, 1) == 4 * (6 - 1) * slot
+    assert size(100, 300, 2, 128, 1 << 24) == size(100, 300, 2, 128, 3)
+    assert size(5000, 5000, 24, 128, 30) == size(900, 5000, 24, 128, 30)     # every SM has its slots
 
 
 def test_contiguous_tensors_are_asked_for():
