@@ -523,6 +523,7 @@ constexpr int kCopyVecs = 4;   // 16-byte vectors of a thread
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(const __grid_constant__ CopyParams p, const __grid_constant__ long long cta0_1,
                 const __grid_constant__ long long cta0_2, int parts0, int parts2) {
+    wait_for_stream();
     long long c = blockIdx.x;
     const int r = c >= cta0_2 ? 2 : c >= cta0_1 ? 1 : 0;
     c -= r == 2 ? cta0_2 : r == 1 ? cta0_1 : 0;
@@ -618,9 +619,8 @@ cudaError_t launch_copy(const CopyParams& p, cudaStream_t s) {
         cta0[r + 1] = cta0[r] + parts[r] * p.planes * p.heads;
     }
     if (cta0[3] >= (1LL << 31) || cta0[3] <= 0) return cudaErrorInvalidConfiguration;
-    copy_kernel<<<(unsigned)cta0[3], kCopyThreads, 0, s>>>(p, cta0[1], cta0[2], (int)parts[0],
-                                                           (int)std::max(1LL, parts[2]));
-    return cudaGetLastError();
+    return launch_early(copy_kernel, (unsigned)cta0[3], kCopyThreads, 0, 1, s, p, cta0[1], cta0[2],
+                        (int)parts[0], (int)std::max(1LL, parts[2]));
 }
 
 }  // namespace pv
