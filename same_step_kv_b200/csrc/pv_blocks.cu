@@ -280,8 +280,8 @@ __device__ void write_top(const unsigned long long* keys, int n, int n_sel, SelS
 }
 
 // The n_sel best of n blocks, as ascending indices; -1 up to keep.  keys
-// holds f32 scores, each off by at most `err`, on entry, f64 scores if they
-// are needed.  Blocks whose f32 score is more than 2 err above the n_sel-th
+// holds f32 scores, each finite and off by at most `err` unless that is
+// infinite, on entry, f64 scores if they are needed.  Blocks whose f32 score is more than 2 err above the n_sel-th
 // largest one are among the best whatever the errors, those more than 2 err
 // below are not, and the few between (seldom more than one) are scored in
 // f64 by score(b), eight lanes of a warp to a block.
@@ -293,14 +293,15 @@ __device__ void choose(unsigned long long* keys64, int n, int n_sel, int keep, f
     const uint32_t edge = nth_key(keys, n, n_sel, sh);
     // taken: keys from `above` on; close: keys from `from` up to it
     uint32_t above, from;
-    if (edge >= kForced || edge == 0) {       // forced blocks alone; or NaN at the border
-        above = max(edge, 1u);
-        from = edge;
+    if (edge >= kForced) {                    // forced blocks alone
+        above = from = edge;
+    } else if (!(err < INFINITY)) {           // f32 tells nothing: every unforced block in f64
+        above = kForced;
+        from = 0;
     } else {
         const float at = key_value(edge);
         above = min(order_key(__fadd_ru(at, 2.f * err)), kForced - 1) + 1;
         from = order_key(__fadd_rd(at, -2.f * err));
-        if (!(err < INFINITY)) above = kForced, from = 0;
     }
     int taken = 0, close = 0;
     for (int i0 = 0; i0 < n; i0 += kSelThreads) {
@@ -491,7 +492,10 @@ __global__ void __launch_bounds__(kSelThreads, 4)
     for (int o = 4; o > 0; o /= 2) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
     float err = (2 * kRuns + 8) * 0x1p-24f * (sqrtf(q2) + 1e-18f) *
                     (sqrtf(__uint_as_float(sh.norm2)) + 1e-18f) + 1e-36f;
-    if (!(err < INFINITY)) err = INFINITY;
+    // From 2^100 on, and where a length is infinite or NaN, products or partial
+    // sums may have overflowed and no f32 score is worth anything; below it
+    // |qmean| |kmean| is under 2^121 and every f32 score is finite.
+    if (!(err < 0x1p100f)) err = INFINITY;
     choose(keys64, n, min(p.keep, n), p.keep, err, &sh, p.blocks + (long long)item * p.keep,
            [&](int b) {
                const float4* src = mean_of(b);
