@@ -161,8 +161,11 @@ PV_API pv_status pv_kv_destroy(pv_kv kv);
  *  - pv_rope_append, pv_qkv_rope_append and pv_block_summarize write the
  *    current chunk's page(s) and return PV_ERR_STATE while another stream
  *    holds them too.
- *  - pv_kv_set_state keeps the pages of frames that stay and takes free ones
- *    for the others (contents are the caller's to restore).
+ *  - pv_kv_set_state keeps the pages of frames that stay, shared or not; a
+ *    slot that gets another frame keeps its page only if no other stream
+ *    holds it, and takes a free one otherwise.  Contents are the caller's to
+ *    restore; what other streams hold too is not to be written: release the
+ *    stream first to give it a history that differs.
  *  - pv_chunk_attn reads through the page table, block by block
  *    (PV_BLOCK_KEYS); rows behind a frame's end are never read, and P is
  *    rounded as by pv_block_attn.

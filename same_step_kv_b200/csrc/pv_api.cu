@@ -734,8 +734,8 @@ pv_status pv_kv_set_state(pv_kv kv, int stream, const pv_kv_state* st) {
     std::lock_guard<std::mutex> lock(kv->mu);
     StreamState& old = kv->streams[stream];
     if (kv->n_pages > 0) {
-        // keep the pages of segments that stay, take free ones for the others;
-        // on failure give those back
+        // keep the pages of frames that stay and, for other frames, those that
+        // no other stream holds; free ones for the rest, given back on failure
         s.sink_page = s.phase == PV_PHASE_NEW ? -1 : old.sink_page;
         int fresh[PV_MAX_RING], n_fresh = 0;
         int fresh_sink = -1;
@@ -749,8 +749,11 @@ pv_status pv_kv_set_state(pv_kv kv, int stream, const pv_kv_state* st) {
         }
         int want = ok ? 1 : c.first_frames;
         for (int i = 0; ok && i < s.fill; ++i) {
-            s.page[i] = old.page[i];
-            if (s.page[i] >= 0) continue;
+            const int was = old.page[i];
+            if (was >= 0 && (kv->ref[was] == 1 || old.slot_frame[i] == s.slot_frame[i])) {
+                s.page[i] = was;
+                continue;
+            }
             const int page = find_pages(kv, 1);
             if (!(ok = page >= 0)) break;
             kv->ref[page] = 1;
@@ -765,8 +768,8 @@ pv_status pv_kv_set_state(pv_kv kv, int stream, const pv_kv_state* st) {
         // drop what the new state does not hold
         if (s.sink_page < 0 && old.sink_page >= 0)
             hold_pages(kv, old.sink_page, c.first_frames, -1);
-        for (int i = s.fill; i < c.ring_slots; ++i)
-            if (old.page[i] >= 0) --kv->ref[old.page[i]];
+        for (int i = 0; i < c.ring_slots; ++i)
+            if (old.page[i] >= 0 && old.page[i] != s.page[i]) --kv->ref[old.page[i]];
     }
     old = s;
     return PV_OK;
