@@ -202,7 +202,11 @@ PV_API pv_status pv_kv_release(pv_kv kv, int stream);
  * order, so that the free ones form one run (a first chunk needs F0
  * consecutive ones).  Keys, and block means where attached, are moved on
  * cuda_stream and every stream's page table follows; *moved (optional)
- * counts the pages moved.  Fixed rows: nothing to do. */
+ * counts the pages moved.  Fixed rows: nothing to do.
+ * A launch takes 480 moves.  If the first one fails (PV_ERR_CUDA), nothing
+ * has changed; if a later one fails, pages have moved and others have not:
+ * the streams that hold a page behind the first free one are then ended as
+ * by pv_kv_release, the others go on. */
 PV_API pv_status pv_kv_compact(pv_kv kv, int* moved, void* cuda_stream);
 
 /* Pages of `stream`: the first of the sink's F0 consecutive ones and

@@ -1334,15 +1334,30 @@ pv_status pv_kv_compact(pv_kv kv, int* moved, void* cuda_stream) {
         if ((st = check_async("an earlier launch"))) return st;
     }
     std::lock_guard<std::mutex> lock(kv->mu);
-    int live = 0, n_moved = 0;
+    int live = 0, n_moved = 0, n_queued = 0, first = -1;
     CopyParams p{};
     p.len = 1;
     if (kv->device) copy_regions(kv, &p);
-    auto flush = [&]() -> cudaError_t {
+    auto flush = [&]() -> pv_status {
         const cudaError_t e =
             kv->device && p.n > 0 ? launch_copy(p, (cudaStream_t)cuda_stream) : cudaSuccess;
-        p.n = 0;
-        return e;
+        if (e == cudaSuccess) {
+            n_queued += p.n;
+            p.n = 0;
+            return PV_OK;
+        }
+        // earlier launches may have moved pages, over others' old places:
+        // whoever holds a page from the first gap on has lost its keys
+        if (n_queued > 0)
+            for (StreamState& s : kv->streams) {
+                bool lost = s.sink_page >= 0 && s.sink_page + kv->cfg.first_frames > first;
+                for (int r = 0; r < kv->cfg.ring_slots; ++r) lost = lost || s.page[r] >= first;
+                if (!lost) continue;
+                release_pages(kv, s);
+                s = StreamState();
+            }
+        return cuda_fail(e, n_queued > 0 ? "compaction launch (streams behind the first gap are lost)"
+                                         : "compaction launch");
     };
     // held pages slide down in ascending order: a run of consecutive ones
     // (a sink) stays one
@@ -1350,18 +1365,15 @@ pv_status pv_kv_compact(pv_kv kv, int* moved, void* cuda_stream) {
         if (kv->ref[i] == 0) continue;
         kv->remap[i] = live;
         if (live != i) {
+            if (first < 0) first = i;
             p.src[p.n] = i;
             p.dst[p.n] = live;
             ++n_moved;
-            if (++p.n == kMaxMoves) {
-                const cudaError_t e = flush();
-                if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
-            }
+            if (++p.n == kMaxMoves && (st = flush())) return st;
         }
         ++live;
     }
-    const cudaError_t e = flush();
-    if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
+    if ((st = flush())) return st;
     for (int i = 0; i < kv->n_pages; ++i)
         if (kv->ref[i] > 0 && kv->remap[i] != i) {
             kv->ref[kv->remap[i]] = kv->ref[i];
