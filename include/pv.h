@@ -330,8 +330,10 @@ PV_API pv_status pv_chunk_attn(pv_kv kv, int n_streams, const int* streams, int 
  * [(F0 + R) * bps][D], for a paged store [layers][steps][H][n_pages * bps][D]. */
 PV_API pv_status pv_kv_summary_bytes(pv_kv kv, size_t* bytes);
 /* Attaches (NULL: detaches) a caller-owned buffer for the block means,
- * 256-byte aligned, and zero-fills it (synchronous).  Until the handle is
- * destroyed or the buffer detached, pv_block_summarize and page copies write it. */
+ * 256-byte aligned, and zero-fills it on the default stream (synchronous:
+ * complete when the call returns; earlier work on the buffer must have ended).
+ * Until the handle is destroyed or the buffer detached, pv_block_summarize and
+ * page copies write it. */
 PV_API pv_status pv_kv_set_summaries(pv_kv kv, void* summ_dev, size_t bytes);
 
 /* Mean key of every block that the listed streams' current chunks hold at

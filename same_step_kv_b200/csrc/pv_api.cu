@@ -1432,7 +1432,10 @@ pv_status pv_kv_set_summaries(pv_kv kv, void* summ_dev, size_t bytes) {
         if (!aligned(summ_dev, 256))
             return fail(PV_ERR_INVALID_ARG, "block means must be 256-byte aligned");
         if ((st = check_same_device(kv))) return st;
-        const cudaError_t e = cudaMemset(summ_dev, 0, need);
+        // (a memset of device memory returns before it has run, and a stream made
+        // without blocking does not wait for the default stream)
+        cudaError_t e = cudaMemset(summ_dev, 0, need);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
         if (e != cudaSuccess) return cuda_fail(e, "clearing the block means");
     }
     std::lock_guard<std::mutex> lock(kv->mu);

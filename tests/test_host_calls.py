@@ -154,3 +154,29 @@ def test_fork_whose_copy_fails_changes_nothing(lib, pages):
     assert lib.pv_kv_fork(s.h, 0, 2, dst, 1, None) == pv.PV_OK
     assert log(lib) == ["launch copy"] and s.state(3) == s.state(0)
     lib.pv_kv_destroy(s.h)
+
+
+# ------------------------------------------------------------------ set-up calls are complete when they return
+def waits_after(lines, what):
+    """Whether the log holds a wait behind the last line that begins with `what`."""
+    last = max(i for i, x in enumerate(lines) if x.startswith(what))
+    return any(x.startswith("wait") for x in lines[last + 1:])
+
+
+@pytest.mark.parametrize("pages", [None, 12])
+def test_attached_means_are_clear_when_the_call_returns(lib, pages):
+    """Calls on a stream that does not wait for the default one may follow at once."""
+    s = Store(lib, pv.make_config(1, 2, 64, 4, 4, first_frames=F0, ring_slots=3, steps=2, max_streams=2,
+                                  max_frames=64), pages)
+    n = ctypes.c_size_t()
+    assert lib.pv_kv_summary_bytes(s.h, ctypes.byref(n)) == pv.PV_OK
+    lib.fake_reset(-1)
+    assert lib.pv_kv_set_summaries(s.h, MEANS, n.value) == pv.PV_OK
+    assert waits_after(log(lib), "memset")
+    assert lib.pv_kv_begin_chunk(s.h, 0, F0) == pv.PV_OK
+    ids = (ctypes.c_int * 1)(0)
+    lib.fake_reset(-1)
+    assert lib.pv_block_summarize(s.h, 1, ids, 0, 0, 77) == pv.PV_OK
+    assert lib.pv_kv_set_summaries(s.h, None, 0) == pv.PV_OK
+    assert log(lib) == ["launch means"]
+    lib.pv_kv_destroy(s.h)
