@@ -475,8 +475,8 @@ class KVStore:
             self.kv_bytes, self.ws_bytes = pv_kv_required_bytes(cfg)
         else:
             self.kv_bytes, self.ws_bytes = pv_kv_paged_required_bytes(cfg, pages)
-        self.kv_buf = torch.empty(self.kv_bytes, dtype=torch.uint8, device=device)
-        self.ws_buf = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.kv_buf = self._alloc(self.kv_bytes, device)
+        self.ws_buf = self._alloc(self.ws_bytes, device)
         bufs = (self.kv_buf, self.kv_bytes, self.ws_buf, self.ws_bytes)
         self.handle = pv_kv_init(cfg, *bufs) if pages is None else pv_kv_init_paged(cfg, pages, *bufs)
         self.T = cfg.frame_w * cfg.frame_h
@@ -484,10 +484,19 @@ class KVStore:
         self.summ_buf = self._summ = None
         if summaries:
             n = pv_kv_summary_bytes(self.handle)
-            self.summ_buf = torch.empty(n, dtype=torch.uint8, device=device)
+            self.summ_buf = self._alloc(n, device)
             pv_kv_set_summaries(self.handle, self.summ_buf, n)
             rows = self.ltot // self.T * -(-self.T // PV_BLOCK_KEYS)
             self._summ = self.summ_buf.view(torch.float32).view(self._shape(rows))
+
+    @staticmethod
+    def _alloc(n, device):
+        """n bytes that nothing uses any more: the allocator may hand out memory that work of the
+        current stream still writes, and the library clears it on the default stream."""
+        import torch
+        t = torch.empty(n, dtype=torch.uint8, device=device)
+        torch.cuda.current_stream(t.device).synchronize()
+        return t
 
     def _shape(self, rows):
         """[layers][steps][streams][heads][rows][D], without streams for a paged store."""

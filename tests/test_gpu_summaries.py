@@ -46,3 +46,26 @@ def test_means_written_right_after_attaching_stay(pv, pages):
         pv.pv_kv_set_summaries(h, None)
         buf.fill_(255)
     store.close()
+
+
+def test_a_store_made_on_a_busy_stream(pv):
+    """Memory that the allocator hands out again while work of the current stream still writes it."""
+    side = torch.cuda.Stream()
+    cfg = pv.make_config(1, 4, 128, 20, 15, ring_slots=2, steps=1, max_streams=1, max_frames=64)
+    a = torch.randn(8192, 8192, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        first = pv.KVStore(cfg, summaries=True)
+        sizes = first.kv_bytes, first.ws_bytes, first.summ_buf.numel()
+        b = torch.empty_like(a)
+        for _ in range(30):
+            torch.matmul(a, a, out=b)
+        junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        for t in junk:
+            t.fill_(255)
+        del junk, t
+        made = pv.KVStore(cfg, summaries=True)
+        torch.cuda.synchronize()
+        assert (made.summary_region() == 0).all()
+        assert (made.k_region() == 0).all() and (made.v_region() == 0).all()
+    first.close(), made.close()
