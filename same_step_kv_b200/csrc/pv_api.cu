@@ -531,6 +531,8 @@ pv_status store_init(pv_kv* out, const pv_kv_config* cfg, int n_pages, void* kv_
         if (e == cudaSuccess)
             e = cudaMemcpy(kv->ws + kv->wl.tab_off, tab.data(), sizeof(float2) * tab.size(),
                            cudaMemcpyHostToDevice);
+        // (a copy from pageable memory may return once it is staged)
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
         if (e != cudaSuccess) {
             delete kv;
             return cuda_fail(e, "initialising the store");

@@ -180,3 +180,14 @@ def test_attached_means_are_clear_when_the_call_returns(lib, pages):
     assert lib.pv_kv_set_summaries(s.h, None, 0) == pv.PV_OK
     assert log(lib) == ["launch means"]
     lib.pv_kv_destroy(s.h)
+
+
+@pytest.mark.parametrize("pages", [None, 12])
+def test_a_store_is_ready_when_the_call_returns(lib, pages):
+    """The zero fill and the RoPE table (copied from pageable memory, which may return before the
+    copy has reached the device)."""
+    Store(lib, pv.make_config(1, 2, 64, 4, 4, first_frames=F0, ring_slots=3, steps=2, max_streams=2,
+                              max_frames=64), pages)
+    lines = log(lib)
+    assert lines.count("memset") == 2 and "memcpy" in lines
+    assert waits_after(lines, "memset") and waits_after(lines, "memcpy")
