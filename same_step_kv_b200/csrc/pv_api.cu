@@ -1653,6 +1653,7 @@ pv_status pv_block_select_dense(const void* q, const float* means, int n_q, int 
 
 pv_status pv_block_attn_dense_ws_bytes(int n_q, int n_k, int heads, int head_dim, int keep,
                                        size_t* ws_bytes) {
+    if (!ws_bytes) return fail(PV_ERR_INVALID_ARG, "output pointer is NULL");
     int nb = 0;
     pv_status st = dense_blocks(n_q, n_k, heads, head_dim, &nb);
     if (st) return st;

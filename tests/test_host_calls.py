@@ -5,6 +5,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -191,3 +192,51 @@ def test_a_store_is_ready_when_the_call_returns(lib, pages):
     lines = log(lib)
     assert lines.count("memset") == 2 and "memcpy" in lines
     assert waits_after(lines, "memset") and waits_after(lines, "memcpy")
+
+
+# ------------------------------------------------------------------ NULL outputs
+NULLS = {
+    "pv_block_attn_dense_ws_bytes": "lib.pv_block_attn_dense_ws_bytes(5, 300, 2, 64, 2, None)",
+    "pv_attn_dense_ws_bytes": "lib.pv_attn_dense_ws_bytes(5, 300, 2, 64, None)",
+    "pv_kv_paged_required_bytes": "lib.pv_kv_paged_required_bytes(byref(cfg), 9, None, None)",
+    "pv_kv_paged_required_bytes, config": "lib.pv_kv_paged_required_bytes(None, 9, None, None)",
+    "pv_kv_init_paged": "lib.pv_kv_init_paged(None, byref(cfg), 9, None, 0, None, 0)",
+    "pv_kv_init_paged, config": "lib.pv_kv_init_paged(byref(h), None, 9, None, 0, None, 0)",
+    "pv_kv_summary_bytes": "lib.pv_kv_summary_bytes(h, None)",
+    "pv_kv_free_pages": "lib.pv_kv_free_pages(h, None, None)",
+    "pv_kv_page_table": "lib.pv_kv_page_table(h, 0, None, None)",
+    "pv_kv_get_state": "lib.pv_kv_get_state(h, 0, None)",
+    "pv_kv_set_state": "lib.pv_kv_set_state(h, 0, None)",
+    "pv_kv_row_offset": "lib.pv_kv_row_offset(h, 0, 0, 0, 0, 0, None, None)",
+    "pv_kv_fork": "lib.pv_kv_fork(h, 0, 1, None, 0, None)",
+    "pv_block_summarize": "lib.pv_block_summarize(dev, 1, None, 0, 0, None)",
+    "pv_block_select": "lib.pv_block_select(dev, 1, None, 0, 0, 256, 2, 0, 256, None)",
+    "pv_block_select, tensors": "lib.pv_block_select(dev, 1, one, 0, 0, None, 2, 0, None, None)",
+    "pv_block_attn": "lib.pv_block_attn(dev, 1, None, 0, 0, 256, 256, 2, 256, None, None)",
+    "pv_block_attn, tensors": "lib.pv_block_attn(dev, 1, one, 0, 0, None, 256, 2, None, None, None)",
+    "pv_chunk_attn": "lib.pv_chunk_attn(dev, 1, None, 0, 0, 256, 256, None, None)",
+}
+
+
+@pytest.mark.parametrize("name", NULLS)
+def test_null_pointers_are_refused(lib, name):
+    """In a process of its own: what takes a NULL pointer for granted ends it."""
+    code = f"""
+import ctypes
+from ctypes import byref
+from same_step_kv_b200 import pv
+lib = ctypes.CDLL({lib.so!r})
+for n, (a, r) in pv._SIGS.items():
+    if f := getattr(lib, n, None):
+        f.argtypes, f.restype = a, r
+cfg = pv.make_config(1, 2, 64, 4, 4, first_frames=3, ring_slots=3, steps=2, max_streams=2, max_frames=64)
+h, dev = ctypes.c_void_p(), ctypes.c_void_p()
+assert lib.pv_kv_init_paged(byref(h), byref(cfg), 9, None, 0, None, 0) == 0
+assert lib.pv_kv_init_paged(byref(dev), byref(cfg), 9, {KV}, 1 << 62, {WS}, 1 << 62) == 0
+assert lib.pv_kv_set_summaries(dev, {MEANS}, 1 << 62) == 0
+one = (ctypes.c_int * 1)(0)
+assert lib.pv_kv_begin_chunk(h, 0, 3) == 0 and lib.pv_kv_begin_chunk(dev, 0, 3) == 0
+assert {NULLS[name]} == pv.PV_ERR_INVALID_ARG
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, f"{r.returncode} {r.stderr[-500:]}"
