@@ -139,13 +139,19 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _dense(t, size: int) -> int | None:
-    """_ptr of a contiguous CUDA tensor of `size`-byte elements (or an address)."""
+_BF16, _F32, _I32, _BYTES = "torch.bfloat16", "torch.float32", "torch.int32", "torch.uint8"
+_names = {}  # a tensor's type -> its name
+
+
+def _dense(t, kind: str) -> int | None:
+    """_ptr of a contiguous CUDA tensor of type `kind` (bytes: of any one-byte type), or an address."""
     if t is None or isinstance(t, int):
         return t
-    if not (t.is_cuda and t.is_contiguous() and t.element_size() == size):
-        raise PVError(PV_ERR_INVALID_ARG, f"a contiguous CUDA tensor of {size}-byte elements is "
-                                          f"needed, not {tuple(t.shape)} {t.dtype} on {t.device}")
+    name = _names.get(t.dtype) or _names.setdefault(t.dtype, str(t.dtype))
+    if not (t.is_cuda and t.is_contiguous() and
+            (name == kind or kind == _BYTES and t.element_size() == 1)):
+        raise PVError(PV_ERR_INVALID_ARG, f"a contiguous CUDA tensor of {kind} is needed, not "
+                                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -306,26 +312,26 @@ def pv_block_summarize(kv, streams, layer, step, cuda_stream=None) -> None:
 
 def pv_block_select(kv, streams, layer, step, q_rot, keep, force, blocks, cuda_stream=None) -> None:
     n, arr = _streams(streams)
-    _check(lib.pv_block_select(kv, n, arr, layer, step, _dense(q_rot, 2), keep, force, _dense(blocks, 4),
+    _check(lib.pv_block_select(kv, n, arr, layer, step, _dense(q_rot, _BF16), keep, force, _dense(blocks, _I32),
                                _stream(cuda_stream)))
 
 
 def pv_block_attn(kv, streams, layer, step, q_rot, blocks, keep, out, lse=None,
                   cuda_stream=None) -> None:
     n, arr = _streams(streams)
-    _check(lib.pv_block_attn(kv, n, arr, layer, step, _dense(q_rot, 2), _dense(blocks, 4), keep,
-                             _dense(out, 2), _dense(lse, 4), _stream(cuda_stream)))
+    _check(lib.pv_block_attn(kv, n, arr, layer, step, _dense(q_rot, _BF16), _dense(blocks, _I32), keep,
+                             _dense(out, _BF16), _dense(lse, _F32), _stream(cuda_stream)))
 
 
 def pv_block_summarize_dense(k, n_k, heads, head_dim, means, cuda_stream=None) -> None:
-    _check(lib.pv_block_summarize_dense(_dense(k, 2), n_k, heads, head_dim, _dense(means, 4),
+    _check(lib.pv_block_summarize_dense(_dense(k, _BF16), n_k, heads, head_dim, _dense(means, _F32),
                                         _stream(cuda_stream)))
 
 
 def pv_block_select_dense(q, means, n_q, n_k, heads, head_dim, keep, n_front, blocks,
                           cuda_stream=None) -> None:
-    _check(lib.pv_block_select_dense(_dense(q, 2), _dense(means, 4), n_q, n_k, heads, head_dim, keep,
-                                     n_front, _dense(blocks, 4), _stream(cuda_stream)))
+    _check(lib.pv_block_select_dense(_dense(q, _BF16), _dense(means, _F32), n_q, n_k, heads, head_dim, keep,
+                                     n_front, _dense(blocks, _I32), _stream(cuda_stream)))
 
 
 def pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep) -> int:
@@ -336,8 +342,8 @@ def pv_block_attn_dense_ws_bytes(n_q, n_k, heads, head_dim, keep) -> int:
 
 def pv_block_attn_dense(q, k, v, n_q, n_k, heads, head_dim, blocks, keep, out, lse, ws, ws_bytes,
                         cuda_stream=None) -> None:
-    _check(lib.pv_block_attn_dense(_dense(q, 2), _dense(k, 2), _dense(v, 2), n_q, n_k, heads, head_dim,
-                                   _dense(blocks, 4), keep, _dense(out, 2), _dense(lse, 4), _dense(ws, 1),
+    _check(lib.pv_block_attn_dense(_dense(q, _BF16), _dense(k, _BF16), _dense(v, _BF16), n_q, n_k, heads, head_dim,
+                                   _dense(blocks, _I32), keep, _dense(out, _BF16), _dense(lse, _F32), _dense(ws, _BYTES),
                                    ws_bytes, _stream(cuda_stream)))
 
 
