@@ -183,8 +183,9 @@ PV_API pv_status pv_kv_init_paged(pv_kv* out, const pv_kv_config* cfg, int n_pag
  *  copy_current != 0 each branch gets its own copy of the current chunk's
  *  page(s) (the sink's F0 pages while the first chunk or the sink pass is
  *  current), so that src and every branch can go on denoising it.  With 0
- *  the current chunk should be complete; its page is shared until a holder
- *  moves on.
+ *  the current chunk should be complete: its page is shared, so that neither
+ *  src nor a branch can write it again while more than one stream holds it
+ *  (a stream that starts its next chunk still holds it, as history).
  *  Fixed rows: every key that src holds is copied (copy_current is ignored).
  * Block means, where attached, are copied with the keys.  The copies are
  * asynchronous on cuda_stream; calls of the handle issued on another stream
@@ -339,7 +340,9 @@ PV_API pv_status pv_kv_set_summaries(pv_kv kv, void* summ_dev, size_t bytes);
 /* Mean key of every block that the listed streams' current chunks hold at
  * (layer, step), as pv_rope_append wrote them (PV_STEP_SINK: in every step
  * buffer).  The sum of a block is taken in f64 and the mean rounded once to
- * f32.  PV_ERR_STATE without attached means. */
+ * f32.  PV_ERR_STATE without attached means.  Means are not tracked: those of
+ * a frame begun, appended again or restored since are the old ones (zeros, or
+ * the page's former frame's) until this call or the caller writes them. */
 PV_API pv_status pv_block_summarize(pv_kv kv, int n_streams, const int* streams, int layer,
                                     int step, void* cuda_stream);
 

@@ -240,3 +240,20 @@ assert {NULLS[name]} == pv.PV_ERR_INVALID_ARG
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, f"{r.returncode} {r.stderr[-500:]}"
+
+
+def test_a_shared_page_is_written_by_its_last_holder_only(lib):
+    """A branch taken with its current page shared: starting the next chunk does not give the page up."""
+    s = Store(lib, pv.make_config(1, 2, 64, 4, 4, first_frames=F0, ring_slots=3, steps=2, max_streams=2,
+                                  max_frames=64), 12)
+    s.set(0, 2)
+    one = (ctypes.c_int * 1)(1)
+    append = lambda i: lib.pv_rope_append(s.h, 1, (ctypes.c_int * 1)(i), 0, 0, 256, 256, 256, 256, None)  # noqa: E731
+    assert append(0) == pv.PV_OK
+    assert lib.pv_kv_fork(s.h, 0, 1, one, 0, None) == pv.PV_OK
+    assert append(0) == append(1) == pv.PV_ERR_STATE
+    assert lib.pv_kv_begin_chunk(s.h, 0, 1) == pv.PV_OK
+    assert append(0) == pv.PV_OK and append(1) == pv.PV_ERR_STATE
+    assert lib.pv_kv_release(s.h, 0) == pv.PV_OK
+    assert append(1) == pv.PV_OK
+    lib.pv_kv_destroy(s.h)
