@@ -134,6 +134,10 @@ pv_status check_config(const pv_kv_config* c, int n_pages = 0) {
         rows >= (1LL << 31) || (long long)c->first_frames * T * c->heads >= (1LL << 30))
         return fail(PV_ERR_SHAPE, "store of %lld rows exceeds the 2^31 rows a tensor map addresses",
                     rows);
+    const long long max_qb = ((long long)c->first_frames * T + kQBlock - 1) / kQBlock;
+    if ((long long)c->max_streams * c->heads * max_qb * kQTilesPerCta >= (1LL << 31))
+        return fail(PV_ERR_SHAPE, "%d streams of %d heads and %lld query blocks: too many in a launch",
+                    c->max_streams, c->heads, max_qb);
     if (c->first_frames - 1 + 1 > c->max_frames)
         return fail(PV_ERR_SHAPE, "max_frames %d smaller than first_frames", c->max_frames);
     return PV_OK;

@@ -98,3 +98,19 @@ def test_a_stream_with_no_history_takes_pages_of_its_own():
     set_chunk(h, 1, -1, pv.PV_PHASE_NEW)
     assert pv.pv_kv_free_pages(h)[0] == 10
     pv.pv_kv_destroy(h)
+
+
+@pytest.mark.parametrize("heads,fits", [((1 << 24) - 1, True), (1 << 24, False), (1 << 25, False),
+                                        ((1 << 25) + (1 << 18), False)])
+def test_arrival_counters_beyond_32_bits_are_refused(heads, fits):
+    """The streams of a paged store are not bounded by its rows: 64 streams of 2^24 heads would need
+    2^31 counters."""
+    c = pv.make_config(1, heads, 64, 1, 1, first_frames=1, ring_slots=1, steps=1, max_streams=64)
+    if fits:
+        kv, ws = pv.pv_kv_paged_required_bytes(c, 2)
+        assert kv == 2 * heads * 2 * 64 * 2 and ws > 64 * heads * 2 * 4
+        return
+    for call in (lambda: pv.pv_kv_paged_required_bytes(c, 2), lambda: pv.pv_kv_init_paged(c, 2)):
+        with pytest.raises(pv.PVError) as e:
+            call()
+        assert e.value.status == pv.PV_ERR_SHAPE
