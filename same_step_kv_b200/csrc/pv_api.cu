@@ -32,7 +32,10 @@ pv_status fail(pv_status code, const char* fmt, ...) {
     return code;
 }
 
+// Reports a failed CUDA call, and takes its error off the runtime, so that the
+// next call of the library does not report it again as an earlier launch's.
 pv_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();
     return fail(PV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

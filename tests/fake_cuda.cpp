@@ -14,6 +14,7 @@ namespace {
 std::string g_log;
 int g_copies = 0;            // page-copy launches since fake_reset
 int g_fail_copy = -1;        // the one that fails
+cudaError_t g_last = cudaSuccess;   // what a failed call leaves behind for cudaGetLastError
 std::vector<int> g_moves;    // (src, dst) pairs of the launches that went through
 
 void note(const char* fmt, ...) {
@@ -53,7 +54,11 @@ cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** fn, unsigned, u
     return cudaSuccess;
 }
 const char* cudaGetErrorString(cudaError_t) { return "made up"; }
-cudaError_t cudaGetLastError(void) { return cudaSuccess; }
+cudaError_t cudaGetLastError(void) {
+    const cudaError_t e = g_last;
+    g_last = cudaSuccess;
+    return e;
+}
 cudaError_t cudaMemset(void*, int, size_t) { return note("memset"), cudaSuccess; }
 cudaError_t cudaMemsetAsync(void*, int, size_t, cudaStream_t) { return note("memset async"), cudaSuccess; }
 cudaError_t cudaMemcpy(void*, const void*, size_t, cudaMemcpyKind) { return note("memcpy"), cudaSuccess; }
@@ -82,7 +87,7 @@ cudaError_t launch_few(const FewArgs<PageTable>&, int, int, cudaStream_t) { retu
 cudaError_t launch_summary(const SummaryParams&, cudaStream_t) { return launched("means"); }
 cudaError_t launch_select(const SelectParams&, const PageTable*, cudaStream_t) { return launched("selection"); }
 cudaError_t launch_copy(const CopyParams& p, cudaStream_t) {
-    if (g_copies++ == g_fail_copy) return cudaErrorLaunchOutOfResources;
+    if (g_copies++ == g_fail_copy) return g_last = cudaErrorLaunchOutOfResources;
     for (int i = 0; i < p.n; ++i) {
         g_moves.push_back(p.fan ? p.src[0] : p.src[i]);
         g_moves.push_back(p.dst[i]);

@@ -257,3 +257,16 @@ def test_a_shared_page_is_written_by_its_last_holder_only(lib):
     assert lib.pv_kv_release(s.h, 0) == pv.PV_OK
     assert append(1) == pv.PV_OK
     lib.pv_kv_destroy(s.h)
+
+
+def test_a_failed_launch_is_reported_once(lib):
+    """The call after it is judged by itself."""
+    s = Store(lib, pv.make_config(1, 2, 64, 4, 4, first_frames=F0, ring_slots=3, steps=2, max_streams=2,
+                                  max_frames=64), 12)
+    s.set(0, 2)
+    lib.fake_reset(0)
+    dst = (ctypes.c_int * 1)(1)
+    assert lib.pv_kv_fork(s.h, 0, 1, dst, 1, None) == pv.PV_ERR_CUDA
+    assert lib.pv_chunk_attn(s.h, 1, (ctypes.c_int * 1)(0), 0, 0, 256, 256, None, None) == pv.PV_OK
+    assert log(lib) == ["launch block attention"]
+    lib.pv_kv_destroy(s.h)
