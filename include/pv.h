@@ -138,10 +138,10 @@ PV_API pv_status pv_kv_required_bytes(const pv_kv_config* cfg, size_t* kv_bytes,
 
 /* Creates a handle over caller buffers.  Checks cfg (D in {64,128}, RoPE
  * pairs summing to D/2, 1 <= R <= PV_MAX_RING, ...), checks that the current
- * device is sm_100, builds the RoPE table on the host in fp64, uploads it
- * (synchronous cudaMemcpy) and zero-fills the store and the workspace
- * (synchronous cudaMemset), so that unused key rows hold zeros.  All streams
- * start in PV_PHASE_NEW.
+ * device is sm_100 and holds both buffers, builds the RoPE table on the host
+ * in fp64, uploads it (synchronous cudaMemcpy) and zero-fills the store and
+ * the workspace (synchronous cudaMemset), so that unused key rows hold zeros.
+ * All streams start in PV_PHASE_NEW.
  * Passing kv_dev == NULL and ws_dev == NULL makes a bookkeeping-only handle:
  * no device is touched, the schedule calls work, kernel calls return
  * PV_ERR_STATE.  The handle is freed by pv_kv_destroy. */

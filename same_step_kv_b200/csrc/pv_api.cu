@@ -174,6 +174,20 @@ pv_status check_device(int* n_sm) {
     return PV_OK;
 }
 
+// Device memory lies on the current device (other kinds of memory pass).
+pv_status check_on_device(const void* p, const char* what) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    cudaPointerAttributes a{};
+    e = cudaPointerGetAttributes(&a, p);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    if (a.type == cudaMemoryTypeDevice && a.device != dev)
+        return fail(PV_ERR_INVALID_ARG, "%s: memory of device %d, the current device is %d", what,
+                    a.device, dev);
+    return PV_OK;
+}
+
 }  // namespace
 
 namespace pv {
@@ -509,7 +523,8 @@ pv_status store_init(pv_kv* out, const pv_kv_config* cfg, int n_pages, void* kv_
             delete kv;
             return fail(PV_ERR_INVALID_ARG, "device buffers must be 256-byte aligned");
         }
-        if ((st = check_device(&kv->n_sm))) {
+        if ((st = check_device(&kv->n_sm)) || (st = check_on_device(kv_dev, "the store")) ||
+            (st = check_on_device(ws_dev, "the workspace"))) {
             delete kv;
             return st;
         }
@@ -1440,7 +1455,8 @@ pv_status pv_kv_set_summaries(pv_kv kv, void* summ_dev, size_t bytes) {
             return fail(PV_ERR_CAPACITY, "block means of %zu bytes, need %zu", bytes, need);
         if (!aligned(summ_dev, 256))
             return fail(PV_ERR_INVALID_ARG, "block means must be 256-byte aligned");
-        if ((st = check_same_device(kv))) return st;
+        if ((st = check_same_device(kv)) || (st = check_on_device(summ_dev, "the block means")))
+            return st;
         // (a memset of device memory returns before it has run, and a stream made
         // without blocking does not wait for the default stream)
         cudaError_t e = cudaMemset(summ_dev, 0, need);

@@ -43,6 +43,13 @@ cudaError_t cudaGetDevice(int* dev) {
     *dev = 0;
     return cudaSuccess;
 }
+// addresses from 2^50 on lie on device 1
+cudaError_t cudaPointerGetAttributes(cudaPointerAttributes* a, const void* p) {
+    *a = cudaPointerAttributes{};
+    a->type = cudaMemoryTypeDevice;
+    a->device = ((uintptr_t)p >> 50) != 0;
+    return cudaSuccess;
+}
 cudaError_t cudaDeviceGetAttribute(int* value, cudaDeviceAttr attr, int) {
     *value = attr == cudaDevAttrComputeCapabilityMajor ? 10 : attr == cudaDevAttrMultiProcessorCount ? 148 : 0;
     return cudaSuccess;

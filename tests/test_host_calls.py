@@ -270,3 +270,23 @@ def test_a_failed_launch_is_reported_once(lib):
     assert lib.pv_chunk_attn(s.h, 1, (ctypes.c_int * 1)(0), 0, 0, 256, 256, None, None) == pv.PV_OK
     assert log(lib) == ["launch block attention"]
     lib.pv_kv_destroy(s.h)
+
+
+@pytest.mark.parametrize("pages", [None, 12])
+def test_buffers_of_another_device_are_refused(lib, pages):
+    """Kernels go to the current device: one that reads another's memory would fault."""
+    cfg = pv.make_config(1, 2, 64, 4, 4, first_frames=F0, ring_slots=3, steps=2, max_streams=2, max_frames=64)
+    far, big = 1 << 50, 1 << 62
+    for kv, ws in ((KV + far, WS), (KV, WS + far), (KV + far, WS + far)):
+        lib.fake_reset(-1)
+        h = ctypes.c_void_p(1)
+        st = (lib.pv_kv_init(ctypes.byref(h), ctypes.byref(cfg), kv, big, ws, big) if pages is None else
+              lib.pv_kv_init_paged(ctypes.byref(h), ctypes.byref(cfg), pages, kv, big, ws, big))
+        assert st == pv.PV_ERR_INVALID_ARG and not h.value and log(lib) == []
+    s = Store(lib, cfg, pages)
+    lib.fake_reset(-1)
+    assert lib.pv_kv_set_summaries(s.h, MEANS + far, big) == pv.PV_ERR_INVALID_ARG and log(lib) == []
+    assert lib.pv_kv_begin_chunk(s.h, 0, F0) == pv.PV_OK
+    assert lib.pv_block_summarize(s.h, 1, (ctypes.c_int * 1)(0), 0, 0, None) == pv.PV_ERR_STATE
+    assert lib.pv_kv_set_summaries(s.h, MEANS, big) == pv.PV_OK
+    lib.pv_kv_destroy(s.h)
